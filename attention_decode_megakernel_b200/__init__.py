@@ -55,6 +55,18 @@ class mk_weights(C.Structure):
                 ("layers", C.POINTER(mk_layer_weights))]
 
 
+class mk_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float),
+                ("turns", C.c_double * 128)]
+
+
+class mk_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("pos_stride", C.c_int64), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
+
+
 _lib = None
 
 
@@ -95,6 +107,20 @@ def lib():
             "mk_debug_gemm_noalloc": (C.c_int, [vp, vp, vp, C.c_int, C.c_int, C.c_int, vp]),
             "mk_quantize_w4": (C.c_int, [vp, C.c_int, C.c_int, vp, vp, vp]),
             "mk_gemv_w4": (C.c_int, [vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]),
+            "mk_rope_init": (C.c_int, [C.POINTER(mk_rope), C.c_int, C.c_int, C.c_double, C.c_int,
+                                       C.c_double, C.c_double, C.c_double, C.c_double]),
+            "mk_qk_norm_rope": (C.c_int, [vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, i64,
+                                          vp, i64, i64, C.c_int, C.c_int, C.c_int, C.c_int,
+                                          C.c_float, C.c_int, vp]),
+            "mk_kv_write": (C.c_int, [vp, vp, i64, i64, vp, i64, i64, vp, C.c_int, C.c_int, vp]),
+            "mk_kv_read": (C.c_int, [vp, vp, C.c_int, vp, i64, i64, vp, i64, i64, C.c_int, vp]),
+            "mk_attn_ws_bytes": (sz, [C.c_int]),
+            "mk_attn_paged": (C.c_int, [vp, vp, i64, i64, vp, C.c_int, vp, vp, vp, i64, i64, vp,
+                                        C.c_int, C.c_int, C.c_int, C.c_float, C.c_int, vp, sz,
+                                        vp]),
+            "mk_attn_packed": (C.c_int, [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64,
+                                         i64, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                         C.c_float, C.c_int, vp, sz, vp]),
             "mk_strerror": (C.c_char_p, [C.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -345,3 +371,223 @@ def gemv_w4(codes, scales, x, y, stream=None):
     st = stream if stream is not None else 0
     _check(lib().mk_gemv_w4(_ptr(codes), _ptr(scales), _ptr(x), int(T), int(rows), int(cols),
                             _ptr(y), st), "mk_gemv_w4")
+
+
+# ---- an attention layer over a paged cache ------------------------------------
+#
+# Tensors are device tensors; rows are [token][head][dim] views with any token
+# and head distance (a slice of a fused projection, say).  Without `stream` a
+# call runs on torch's current stream of the tensors' device.
+
+_DTYPES = {}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+
+
+def _dtype(t, what):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2,
+                        torch.float8_e4m3fn: 3})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s: %s is not a supported type" % (what, t.dtype))
+    return code
+
+
+def _rows(t, what, shape=None, like=None):
+    """(pointer, token distance, head distance) of a [token][head][dim] view."""
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s must be [token][head][dim]%s, got %s"
+                         % (what, "" if shape is None else " = %s" % (shape,), tuple(t.shape)))
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError("%s must have the type and device of the other rows" % what)
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise ValueError("the dims of a head of %s must lie side by side" % what)
+    # a distance that is never walked is whatever torch left there
+    return t.data_ptr(), ts if t.shape[0] > 1 else 0, hs if t.shape[1] > 1 else 0
+
+
+def _vector(t, what, dtype, shape, like):
+    import torch
+    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != shape or not t.is_contiguous() \
+            or t.device != like.device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (what, dtype, shape, like.device))
+    return t.data_ptr()
+
+
+def _launch(fn, what, device, stream, *args):
+    """Call fn(*args, stream) with the tensors' device current."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("%s: the tensors must be on a CUDA device" % what)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != MK_OK:
+        raise MkError(rc, what)
+
+
+class Rope:
+    """How positions turn the first `rot_dim` values of a head: pairs
+    (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; frequencies
+    theta^(-2i / rot_dim), scaled for contexts beyond `original_ctx` ("linear",
+    "ntk", "yarn", "banded"; see mk_rope_scaling in include/mk.h)."""
+
+    def __init__(self, rot_dim, theta, interleaved=False, scaling="none", factor=1.0,
+                 original_ctx=0.0, low=1.0, high=32.0):
+        if scaling not in _ROPE_SCALINGS:
+            raise ValueError("scaling must be one of %s" % ", ".join(_ROPE_SCALINGS))
+        self.c = mk_rope()
+        _check(lib().mk_rope_init(C.byref(self.c), int(rot_dim), int(bool(interleaved)),
+                                  float(theta), _ROPE_SCALINGS[scaling], float(factor),
+                                  float(original_ctx), float(low), float(high)), "mk_rope_init")
+        self.address = C.addressof(self.c)
+
+
+def qk_norm_rope(rope, q, k, positions, q_out=None, k_out=None, q_gain=None, k_gain=None,
+                 eps=1e-6, stream=None):
+    """RMSNorm (where a gain [head_dim] is given) and rotation of every head of
+    q [tokens][q_heads][head_dim] and k [tokens][kv_heads][head_dim] (or None),
+    by positions int32 [tokens]; in place where no output is given."""
+    q_out = q if q_out is None else q_out
+    tokens, heads, hd = q.shape
+    qp, qts, qhs = _rows(q, "q")
+    op, ots, ohs = _rows(q_out, "q_out", (tokens, heads, hd), q)
+    kp = kts = khs = okp = okts = okhs = kv_heads = 0
+    if k is not None:
+        kv_heads = k.shape[1]
+        k_out = k if k_out is None else k_out
+        kp, kts, khs = _rows(k, "k", (tokens, kv_heads, hd), q)
+        okp, okts, okhs = _rows(k_out, "k_out", (tokens, kv_heads, hd), q)
+    gains = []
+    for g, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if g is not None and (g.dtype != q.dtype or g.shape != (hd,) or g.stride(0) != 1
+                              or g.device != q.device):
+            raise ValueError("%s must be [head_dim] of the rows' type and device" % what)
+        gains.append(None if g is None else g.data_ptr())
+    pos = _vector(positions, "positions", "int32", (tokens,), q)
+    _launch(lib().mk_qk_norm_rope, "mk_qk_norm_rope", q.device, stream, rope.address, qp, qts, qhs,
+            kp, kts, khs, gains[0], gains[1], pos, op, ots, ohs, okp, okts, okhs, tokens, heads,
+            kv_heads, hd, eps, _dtype(q, "q"))
+
+
+class KvCache:
+    """A paged cache over the caller's tensors k and v, views
+    [page][kv_head][position][dim] with the same distances, bfloat16, float16 or
+    float8_e4m3fn; the latter with float32 scales [page][kv_head][position]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype \
+                or k.device != v.device or k.stride(3) != 1:
+            raise ValueError("k and v must be [page][kv_head][position][dim] views alike, "
+                             "dims side by side")
+        n, heads, size, hd = k.shape
+        code = _dtype(k, "cache")
+        for s in (k_scale, v_scale):
+            if (code == 3) != (s is not None):
+                raise ValueError("scales belong to a float8_e4m3fn cache")
+            if s is not None:
+                _vector(s, "scales", "float32", (n, heads, size), k)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kv_heads, self.head_dim, self.page_size, self.device = heads, hd, size, k.device
+        ps, hs, ts = k.stride()[:3]
+        self.c = mk_kv_cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                             ps if n > 1 else 0, hs if heads > 1 else 0, ts, n, size, heads, hd,
+                             code)
+        self.address = C.addressof(self.c)
+
+
+def kv_write(cache, k, v, slots, stream=None):
+    """Rows k, v [tokens][kv_heads][head_dim] (bfloat16, float16 or float32) into
+    the cache: token t to slot slots[t] = page * page_size + position (int64);
+    a slot outside the cache (-1) skips its token."""
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    kp, kts, khs = _rows(k, "k", shape)
+    vp, vts, vhs = _rows(v, "v", shape, k)
+    sp = _vector(slots, "slots", "int64", shape[:1], cache)
+    if k.device != cache.device:
+        raise ValueError("the rows must be on the cache's device")
+    _launch(lib().mk_kv_write, "mk_kv_write", cache.device, stream, cache.address, kp, kts, khs,
+            vp, vts, vhs, sp, shape[0], _dtype(k, "k"))
+
+
+def kv_read(cache, slots, k_out, v_out, stream=None):
+    """The rows of `slots` as values into k_out, v_out [tokens][kv_heads][head_dim];
+    rows of slots outside the cache stay as they were."""
+    shape = (k_out.shape[0], cache.kv_heads, cache.head_dim)
+    kp, kts, khs = _rows(k_out, "k_out", shape)
+    vp, vts, vhs = _rows(v_out, "v_out", shape, k_out)
+    sp = _vector(slots, "slots", "int64", shape[:1], cache)
+    if k_out.device != cache.device:
+        raise ValueError("the rows must be on the cache's device")
+    _launch(lib().mk_kv_read, "mk_kv_read", cache.device, stream, cache.address, sp, shape[0], kp,
+            kts, khs, vp, vts, vhs, _dtype(k_out, "k_out"))
+
+
+def attn_workspace(head_dim, device="cuda"):
+    """A workspace for attn_paged and attn_packed; calls that may overlap (other
+    streams, graphs replayed at once) need one each."""
+    import torch
+    n = int(lib().mk_attn_ws_bytes(int(head_dim)))
+    if n == 0:
+        raise MkError(MK_ERR_UNSUPPORTED, "mk_attn_ws_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _attn_outputs(q, out, lse, workspace):
+    op, ots, ohs = _rows(out, "out", tuple(q.shape), q)
+    lp = None if lse is None else _vector(lse, "lse", "float32", tuple(q.shape[:2]), q)
+    if workspace is None:
+        workspace = attn_workspace(q.shape[2], q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on the rows' device")
+    return op, ots, ohs, lp, workspace
+
+
+def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None, workspace=None,
+               stream=None):
+    """Attention of new tokens over a paged cache: rows cu_q[b] .. cu_q[b+1]-1 of
+    q [rows][q_heads][head_dim] are the newest of sequence b's seq_lens[b] keys,
+    which lie in the pages block_table[b] (int32).  out as q; lse float32
+    [rows][q_heads] or None; scale head_dim ** -0.5 by default.  Rows behind
+    cu_q[-1] stay as they were."""
+    rows, heads, hd = q.shape
+    qp, qts, qhs = _rows(q, "q")
+    batch = seq_lens.shape[0]
+    if hd != cache.head_dim or q.device != cache.device:
+        raise ValueError("q must have the cache's head_dim and device")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][pages]")
+    pages = block_table.shape[1]
+    tp = _vector(block_table, "block_table", "int32", (batch, pages), q)
+    sp = _vector(seq_lens, "seq_lens", "int32", (batch,), q)
+    cp = _vector(cu_q, "cu_q", "int32", (batch + 1,), q)
+    op, ots, ohs, lp, workspace = _attn_outputs(q, out, lse, workspace)
+    _launch(lib().mk_attn_paged, "mk_attn_paged", q.device, stream, cache.address, qp, qts, qhs,
+            tp, pages, sp, cp, op, ots, ohs, lp, rows, batch, heads,
+            hd ** -0.5 if scale is None else scale, _dtype(q, "q"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+
+
+def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, stream=None):
+    """Causal attention of whole prompts packed one after another: rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [rows][q_heads][head_dim] and of k, v
+    [rows][kv_heads][head_dim] are sequence b."""
+    rows, heads, hd = q.shape
+    kv_heads = k.shape[1]
+    qp, qts, qhs = _rows(q, "q")
+    kp, kts, khs = _rows(k, "k", (rows, kv_heads, hd), q)
+    vp, vts, vhs = _rows(v, "v", (rows, kv_heads, hd), q)
+    batch = cu_seqlens.shape[0] - 1
+    cp = _vector(cu_seqlens, "cu_seqlens", "int32", (batch + 1,), q)
+    op, ots, ohs, lp, workspace = _attn_outputs(q, out, lse, workspace)
+    _launch(lib().mk_attn_packed, "mk_attn_packed", q.device, stream, qp, qts, qhs, kp, kts, khs,
+            vp, vts, vhs, cp, op, ots, ohs, lp, rows, batch, heads, kv_heads, hd,
+            hd ** -0.5 if scale is None else scale, _dtype(q, "q"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())

@@ -21,6 +21,7 @@ FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-v",
+    "--threads", "0",  # the sources side by side
 ]
 
 

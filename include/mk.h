@@ -358,6 +358,162 @@ int mk_quantize_w4(const void *W, int rows, int cols, void *codes, float *scales
 int mk_gemv_w4(const void *codes, const float *scales, const float *x, int T,
                int rows, int cols, float *y, void *stream);
 
+/* ---- an attention layer over a paged cache --------------------------------
+ * Five operators for callers that serve many sequences at once (the launch
+ * post's engine holds one): norm and rotation of query and key heads, writing
+ * and reading a paged cache, attention of a few or many new tokens over that
+ * cache, and attention of whole packed prompts.  No engine is needed.  All are
+ * asynchronous on `stream` (a cudaStream_t or NULL), allocate nothing, may be
+ * captured into a CUDA graph, and run on the device that is current, which
+ * must hold every pointer.
+ *
+ * Rows are [token][head][dim] with the dims of a head side by side; `ts` and
+ * `hs` are the distances between tokens and between heads in values (>= 0),
+ * so that a slice of a fused projection's output is a valid argument.  Rows
+ * start on 16-byte boundaries (base pointers and both distances; else
+ * MK_ERR_ARG).  head_dim is 64, 128 or 256 (else MK_ERR_UNSUPPORTED).  A call
+ * with no tokens (or an empty batch) does nothing. */
+typedef enum { MK_BF16 = 0, MK_FP16 = 1, MK_FP32 = 2, MK_E4M3 = 3 } mk_dtype;
+
+typedef enum {
+  MK_ROPE_NONE = 0,   /* f_i = theta^(-2i / rot_dim)                          */
+  MK_ROPE_LINEAR = 1, /* f_i / factor                                        */
+  MK_ROPE_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) for theta   */
+  MK_ROPE_YARN = 3,   /* f_i / factor for the pairs that turn less than `low`
+                         times over original_ctx positions, f_i for those that
+                         turn more than `high` times, a linear ramp over the
+                         pair index between; rotations 0.1 ln(factor) + 1 long */
+  MK_ROPE_BANDED = 4  /* the same two ends, the share of f_i between them
+                         linear in the number of turns: (turns - low) /
+                         (high - low); rotations of length 1                 */
+} mk_rope_scaling;
+
+/* How positions turn a head, filled by mk_rope_init: host memory that the
+ * caller keeps and passes to mk_qk_norm_rope. */
+typedef struct {
+  int32_t rot_dim;      /* rotated values at the front of a head            */
+  int32_t interleaved;  /* pairs (2i, 2i + 1); else (i, i + rot_dim / 2)     */
+  float magnitude;      /* length of the rotation                            */
+  double turns[128];    /* turns per position of pair i: f_i / 2 pi          */
+} mk_rope;
+
+/* Fill *r (host).  rot_dim a multiple of 16, at most 256 (else
+ * MK_ERR_UNSUPPORTED); theta > 1; factor >= 1 where `scaling` uses it;
+ * original_ctx >= 1 and 0 < low < high for YARN and BANDED (else MK_ERR_ARG).
+ * Arguments that `scaling` does not use are ignored. */
+int mk_rope_init(mk_rope *r, int rot_dim, int interleaved, double theta,
+                 int scaling, double factor, double original_ctx, double low,
+                 double high);
+
+/* RMSNorm of every query and key head over its head_dim values, then the
+ * rotation of its first rot_dim values by the token's position (launch post,
+ * kernel bullet list: "fused QKV + RoPE"; head norms as an option):
+ *   y = x rsqrt(mean(x^2) + eps) gain;  (y_a, y_b) of pair i turned by
+ *   positions[token] * turns[i] turns
+ * in fp32 with the angle reduced in double; rounded once, on the way out.
+ *   q, q_out [tokens][q_heads][head_dim], k, k_out [tokens][kv_heads][head_dim]
+ *   device, of `dtype` (MK_BF16, MK_FP16 or MK_FP32); an output may be its
+ *   input (the same pointer and distances), and must not overlap otherwise;
+ *   q_gain, k_gain device [head_dim] of `dtype`, 16-byte aligned; NULL: no
+ *   norm of that side.  kv_heads == 0: k and k_out are ignored.
+ *   positions device int32 [tokens], of any sign.
+ * rot_dim must not exceed head_dim (MK_ERR_ARG). */
+int mk_qk_norm_rope(const mk_rope *rope, const void *q, int64_t q_ts,
+                    int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                    const void *q_gain, const void *k_gain,
+                    const int32_t *positions, void *q_out, int64_t qo_ts,
+                    int64_t qo_hs, void *k_out, int64_t ko_ts, int64_t ko_hs,
+                    int tokens, int q_heads, int kv_heads, int head_dim,
+                    float eps, int dtype, void *stream);
+
+/* A paged cache of keys and values: n_pages pages of page_size positions
+ * (16, 32, 64, 128 or 256; else MK_ERR_UNSUPPORTED), device memory of the
+ * caller.  The row of (page, head, position) starts page * page_stride +
+ * head * head_stride + position * pos_stride values into k and into v, 16-byte
+ * aligned; rows do not overlap.  dtype MK_BF16 or MK_FP16, or MK_E4M3 with one
+ * float scale for each row in k_scale and v_scale, [page][head][position]
+ * without gaps: a row's values are code * scale.  Scales are positive, normal
+ * numbers; mk_kv_write stores powers of two from 2^-64 to 2^120.  An engine's
+ * cache as mk_get_state copies it out is one sequence of such pages (page
+ * stride page_size * head_dim, head stride pos * head_dim) when its length is
+ * a multiple of the page. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page_stride, head_stride, pos_stride;
+  int32_t n_pages, page_size, kv_heads, head_dim, dtype;
+} mk_kv_cache;
+
+/* Write the rows of `tokens` tokens into a cache: token t goes to slot
+ * slots[t] = page * page_size + position (device int64 [tokens]); a slot
+ * outside the cache (-1 for padding) skips its token.  Slots of one call are
+ * distinct: of two tokens with one slot, either may be kept.  k, v device
+ * [tokens][kv_heads][head_dim] of dtype MK_BF16, MK_FP16 or MK_FP32, rounded
+ * to nearest even.  For an e4m3 cache the scale of a row is the least power of
+ * two, 2^-64 at least, that brings its largest magnitude to 448 or below;
+ * NaN stays NaN; a row with an infinity gets the scale 2^120, with which the
+ * largest code reads back as infinity and small values as 0. */
+int mk_kv_write(const mk_kv_cache *cache, const void *k, int64_t k_ts,
+                int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                const int64_t *slots, int tokens, int dtype, void *stream);
+
+/* Read rows back by slot: k and v receive code * scale (or the stored value)
+ * rounded to dtype; the rows of a slot outside the cache stay as they were.
+ * A slot may be read more than once. */
+int mk_kv_read(const mk_kv_cache *cache, const int64_t *slots, int tokens,
+               void *k, int64_t k_ts, int64_t k_hs, void *v, int64_t v_ts,
+               int64_t v_hs, int dtype, void *stream);
+
+/* Bytes of device workspace (256-byte aligned) of the two attention calls
+ * below for a head_dim; 0 for one that is not implemented.  It holds partial
+ * results of one call: calls that may overlap (other streams, graphs that
+ * replay at once) need one each.  Nothing is kept in it between calls and its
+ * content does not matter. */
+size_t mk_attn_ws_bytes(int head_dim);
+
+/* Attention of new tokens over a paged cache (launch post, "Why nobody had
+ * done this yet?": attention layers read a KV cache that grows by a token;
+ * the follow-up post's draft tokens are chunks of a few): sequence b has its
+ * new tokens in rows cu_q[b] .. cu_q[b + 1] - 1 of q and seq_lens[b] keys in
+ * all, its new ones (already written) among them, in pages block_table[b][0],
+ * [1], ...  New token t of T sees the keys 0 .. seq_lens[b] - T + t:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * with products of 16-bit values and sums, maxima and exponentials in fp32;
+ * the weights are rounded to 16 bits before they multiply the values.
+ *   q, out [rows][q_heads][head_dim] device, dtype MK_BF16 or MK_FP16; query
+ *     head h reads key head h / (q_heads / kv_heads); q_heads a multiple of
+ *     the cache's kv_heads; the cache of the same dtype or MK_E4M3
+ *   block_table device int32 [batch][table_stride]; seq_lens device int32
+ *     [batch], held to 0 .. table_stride * page_size; a page number outside
+ *     the cache stands for keys and values of zero
+ *   cu_q device int32 [batch + 1], from 0, not decreasing, at most `rows`;
+ *     rows from cu_q[batch] on are left as they were
+ *   lse device float32 [rows][q_heads] or NULL: the natural logarithm of the
+ *     sum of exp(scale * q . k_j)
+ * A token that sees no key (seq_lens[b] < T - t) gets out = 0, lse = -inf.
+ * What lies behind seq_lens[b] in a page is never part of a result, whatever
+ * its bits; a key that a token does not see within seq_lens[b] must have
+ * finite values.  out must not overlap an input.  Results do not depend on
+ * timing: the same call gives the same bits. */
+int mk_attn_paged(const mk_kv_cache *cache, const void *q, int64_t q_ts,
+                  int64_t q_hs, const int32_t *block_table, int table_stride,
+                  const int32_t *seq_lens, const int32_t *cu_q, void *out,
+                  int64_t o_ts, int64_t o_hs, float *lse, int rows, int batch,
+                  int q_heads, float scale, int dtype, void *workspace,
+                  size_t ws_bytes, void *stream);
+
+/* Causal attention of whole prompts packed one after another (launch post,
+ * results table: prompt processing; kernel bullet list: causal softmax):
+ * sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q, k and v,
+ * and its row t sees the rows 0 .. t.  k, v [rows][kv_heads][head_dim] device
+ * of q's dtype; everything else as mk_attn_paged. */
+int mk_attn_packed(const void *q, int64_t q_ts, int64_t q_hs, const void *k,
+                   int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                   int64_t v_hs, const int32_t *cu_seqlens, void *out,
+                   int64_t o_ts, int64_t o_hs, float *lse, int rows, int batch,
+                   int q_heads, int kv_heads, int head_dim, float scale,
+                   int dtype, void *workspace, size_t ws_bytes, void *stream);
+
 /* Human-readable text of a status code. */
 const char *mk_strerror(int status);
 
