@@ -8,6 +8,7 @@
 #include "mk.h"
 #include "mk_attn.cuh"
 #include "mk_kvcache.cuh"
+#include "mk_paged.cuh"
 #include "mk_rope.cuh"
 
 namespace {
@@ -312,6 +313,66 @@ int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, vo
   return MK_OK;
 }
 
+constexpr int kMaxDevices = 64;
+
+// The current device and its number of multiprocessors.
+int device_sms(int* dev, int* sms) {
+  static int known[kMaxDevices] = {};
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  if (!known[*dev] && cudaDeviceGetAttribute(&known[*dev], cudaDevAttrMultiProcessorCount, *dev) !=
+                          cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  *sms = known[*dev];
+  return MK_OK;
+}
+
+// The join of partial results, launched so that its CTAs are in place when the
+// kernel before it ends.
+template <class T, int HD>
+int launch_join(const mk::at::AttnArgs& a, const mk::at::Partials& p, int ctas, int rows, int tq,
+                cudaStream_t st) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
+  c.blockDim = dim3(mk::at::JOIN_ROWS * 32);
+  c.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  if (cudaLaunchKernelEx(&c, mk::at::join_kernel<T, HD>, a, p, rows, tq) != cudaSuccess) {
+    return launched();
+  }
+  return launched();
+}
+
+template <class T, class C, int HD, int NT>
+int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+  using F = mk::at::FewCfg<C, HD, NT>;
+  auto* kernel = &mk::at::attn_few_kernel<T, C, HD, NT>;
+  static bool done[kMaxDevices] = {};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  int ctas = sms;
+  while (mk::at::partial_bytes(ctas, F::ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
+  const mk::at::Partials p = mk::at::carve(ws, ctas, F::ROWS, HD);
+  const int tq = F::ROWS / a.group;
+  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, 1);
+  const int rc = launched();
+  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, F::ROWS, tq, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -340,21 +401,32 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   a.table = block_table;
   a.table_stride = table_stride;
   a.seq_lens = seq_lens;
+  int dev, sms;
+  rc = device_sms(&dev, &sms);
+  if (rc != MK_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
   unsigned blocks;
   rc = blocks_for((long long)rows * q_heads, 4, &blocks);
   if (rc != MK_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_half_type(dtype, [&](auto t) {
     by_head_dim(cache->head_dim, [&](auto d) {
       using T = typename decltype(t)::type;
       constexpr int HD = decltype(d)::value;
-      if (cache->dtype == MK_E4M3)
+      const bool e8 = cache->dtype == MK_E4M3;
+      if (unit <= 8)
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 1>(a, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 1>(a, workspace, dev, sms, st);
+      else if (unit <= 16)
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 2>(a, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 2>(a, workspace, dev, sms, st);
+      else if (e8)
         mk::at::attn_simple_kernel<T, mk::E4m3, HD, true><<<blocks, 128, 0, st>>>(a);
       else
         mk::at::attn_simple_kernel<T, T, HD, true><<<blocks, 128, 0, st>>>(a);
     });
   });
-  return launched();
+  return rc != MK_OK ? rc : launched();
 }
 
 int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,

@@ -1,0 +1,468 @@
+// mk_paged.cuh -- attention of few query rows over a paged cache: decoding and
+// short drafts, where a unit's rows (new tokens times the heads of the group)
+// are at most 16.
+//
+// The cache's bytes bound it: every K and V row of a (sequence, key head) is
+// read once, for 2 * 8 * NT multiply-adds a value.  So the layout serves the
+// loads.  Each of the four warps walks its own subtiles of 16 keys through a
+// private ring of stages in shared memory, filled by 16-byte cp.async copies
+// that look up the page, leave out what lies behind the sequence (zeros) and
+// place the pieces so that no read has bank conflicts.  No barrier joins the
+// warps until the unit ends, and the ring runs ahead into the next unit.
+//
+// The products run on mma.m16n8k16 with the keys as M: S^T = K Q^T and
+// O^T = V^T P^T, so that 8 rows (N) cost 8 columns, not a tile of 128 rows.
+// At 8 rows the math of a 16-key subtile is 32 instructions against 16 KB of
+// bytes (head_dim 256): a tcgen05 tile of 128 rows would only add latency.
+// A lane reads 16 bytes of a key row for two k-steps (four of 8-bit values);
+// the order of the head's dims inside a step is free as long as Q has the
+// same.  Score columns turn into weight rows by movmatrix.
+//
+// Softmax: m is raised only when a score passes it by 8 (weights up to 2^8
+// fit both 16-bit types, and their rounding is relative), so most subtiles
+// need one vote and no rescaling.  8-bit caches: codes go to fp16, exactly,
+// as do queries after a power of two for each row; the key row's scale
+// multiplies its scores and log2 of the value row's scale is added to them,
+// so that weights stay in fp16's range; their sum is taken without it.
+#pragma once
+#include <type_traits>
+
+#include "mk_split.cuh"
+
+namespace mk {
+namespace at {
+
+constexpr int FEW_WARPS = 4;
+constexpr int FEW_KEYS = 16 * FEW_WARPS;  // keys of a tile: 16 a warp
+constexpr int FEW_THREADS = 32 * FEW_WARPS;
+
+template <class C, int HD, int NT>
+struct FewCfg {
+  static constexpr bool E8 = __is_same(C, E4m3);
+  static constexpr int ROW = HD * (E8 ? 1 : 2);            // bytes of a cache row
+  static constexpr int STAGE = 32 * ROW + (E8 ? 128 : 0);  // 16 keys, 16 values, their scales
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int JOIN = FEW_WARPS * ROWS * (HD + 4) * 4 + FEW_WARPS * ROWS * 8;
+  static constexpr int FIT = (225 * 1024 - JOIN) / (FEW_WARPS * STAGE);
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  static constexpr size_t SMEM = size_t(FEW_WARPS) * STAGES * STAGE + JOIN;
+  static_assert(STAGES >= 2, "the ring needs two stages");
+};
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 4 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(at));
+  return u;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t u;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(at));
+  return u;
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <class M>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (__is_same(M, Bf16)) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Byte offset of 16-byte piece `ch` of row r of a stage whose rows are ROW
+// bytes: the piece's place in its 128-byte line is turned by the row (of two
+// rows to a line: by the line), so that the lanes of every read below (two
+// rows by four pieces, four rows by two pieces, eight rows by one) hit all banks.
+template <int ROW>
+__device__ __forceinline__ uint32_t piece(int r, int ch) {
+  const int line = ROW >= 128 ? r : r >> 1;
+  const uint32_t turn = (((line >> 1) & 3) * 2) ^ ((line & 1) * 5);
+  return ((uint32_t(r) * (ROW / 16) + ch) ^ turn) * 16;
+}
+
+template <class T, class C, int HD, int NT>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+    attn_few_kernel(const __grid_constant__ AttnArgs a, Partials part, int tq, int least) {
+  using F = FewCfg<C, HD, NT>;
+  constexpr bool E8 = F::E8;
+  using M = typename std::conditional<E8, Fp16, T>::type;  // what the products multiply
+  constexpr int ROW = F::ROW, STAGES = F::STAGES, ROWS = F::ROWS;
+  constexpr int STEPS = HD / 16;              // k-steps of a score, m-tiles of the output
+  constexpr int PIECES = HD / (E8 ? 64 : 32);  // 16-byte pieces of a key row a lane reads
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ long long s_per;
+  __shared__ Cursor<FEW_KEYS> s_cursor;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const Line<FEW_KEYS> line{a, tq};
+  if (warp == 0) {
+    long long per;
+    const Cursor<FEW_KEYS> c = find_share<FEW_KEYS>(line, blockIdx.x, gridDim.x, least, per);
+    if (lane == 0) {
+      s_per = per;
+      s_cursor = c;
+      Left none = {0, 0, 0, 0};
+      part.left[blockIdx.x] = none;
+    }
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  Cursor<FEW_KEYS> at = s_cursor, ahead = at;  // where the math is, where the copies are
+  if (at.left <= 0) return;
+  const int per = int(s_per);
+  const uint32_t ring = smem_addr(smem) + warp * (STAGES * F::STAGE);
+  unsigned char* join = smem + FEW_WARPS * STAGES * F::STAGE;
+  float* join_o = reinterpret_cast<float*>(join);                       // [warp][ROWS][HD + 4]
+  float2* join_ml = reinterpret_cast<float2*>(join + FEW_WARPS * ROWS * (HD + 4) * 4);
+
+  // copies of this warp's 16 keys of the tile at `ahead` into stage st
+  auto fetch = [&](int st) {
+    if (ahead.left > 0) {
+      const int key = ahead.j * FEW_KEYS + warp * 16;
+      const int limit = line.limit(ahead.s, ahead.i);
+      if (key < limit) {
+        const int page = a.table[(long long)ahead.b * a.table_stride + (key >> a.c.page_shift)];
+        const bool known = page >= 0 && page < a.c.n_pages;
+        const int off = key & (a.c.page_size - 1);
+        const long long row0 = (known ? page : 0) * a.c.page_stride +
+                               ahead.h * a.c.head_stride + off * a.c.pos_stride;
+        const uint32_t dst = ring + st * F::STAGE;
+        constexpr int CH = ROW / 16;                     // pieces of a row
+        constexpr int RPI = CH >= 32 ? 1 : 32 / CH;      // rows a copy of the warp covers
+        const int ch = lane % (CH < 32 ? CH : 32), r0 = lane / (CH < 32 ? CH : 32);
+        constexpr int B = E8 ? 1 : 2;
+#pragma unroll
+        for (int r = 0; r < 16; r += RPI) {
+          const bool take = known && key + r + r0 < limit;
+          const long long src = (row0 + (take ? r + r0 : 0) * a.c.pos_stride) * B + ch * 16;
+          const uint32_t to = dst + piece<ROW>(r + r0, ch);
+          cp_async16_or_zero(to, a.c.k + src, take);
+          cp_async16_or_zero(to + 16 * ROW, a.c.v + src, take);
+        }
+        if constexpr (E8) {
+          const int r = lane & 15;
+          const bool take = known && key + r < limit;
+          const long long sc =
+              (((long long)(known ? page : 0) * a.c.kv_heads + ahead.h) << a.c.page_shift) + off +
+              (take ? r : 0);
+          cp_async4_or_zero(dst + 32 * ROW + lane * 4, (lane < 16 ? a.c.k_scale : a.c.v_scale) + sc,
+                            take);
+        }
+      }
+      ahead.next(line);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+
+  int stage = 0;
+  while (at.left > 0) {
+    // ---- one segment: the tiles of one unit that lie in this share
+    const Cursor<FEW_KEYS> u = at;
+    const int seg = u.n - u.j < at.left ? u.n - u.j : at.left;
+    // queries: row r is token r / group of the tile, head r % group
+    uint32_t q[NT][STEPS][2];
+    float qs[NT][2];
+    int limit[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g, token = u.i * tq + r / a.group;
+      const bool live = r < tq * a.group && token < u.s.n_new;
+      const unsigned char* src =
+          a.q + ((u.s.first + (live ? token : 0)) * a.q_ts +
+                 (long long)(u.h * a.group + (live ? r % a.group : 0)) * a.q_hs) * 2;
+      float size = 0.f;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+#pragma unroll
+        for (int half = 0; half < (E8 ? 2 : 1); ++half) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (live)
+            w = *reinterpret_cast<const uint4*>(src + ((4 * i + t) * (E8 ? 2 : 1) + half) * 16);
+          const int st = E8 ? 4 * i + 2 * half : 2 * i;
+          q[nt][st][0] = w.x;
+          q[nt][st][1] = w.y;
+          q[nt][st + 1][0] = w.z;
+          q[nt][st + 1][1] = w.w;
+        }
+      }
+      if constexpr (E8 && __is_same(T, Bf16)) {
+        // bf16 to fp16: a power of two brings the row's largest value to [1, 2)
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            size = fmaxf(size, fmaxf(fabsf(bf_lo(q[nt][i][j])), fabsf(bf_hi(q[nt][i][j]))));
+        size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, 1));
+        size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, 2));
+        uint32_t e = __float_as_uint(size) >> 23;
+        e = e < 1 ? 1 : e > 253 ? 253 : e;
+        const float down = __uint_as_float((254 - e) << 23);
+        size = __uint_as_float(e << 23);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            q[nt][i][j] = RowType<Fp16>::pack2(bf_lo(q[nt][i][j]) * down,
+                                               bf_hi(q[nt][i][j]) * down);
+      } else {
+        size = 1.f;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // the rows 2t, 2t + 1 whose scores this lane holds
+        const int r2 = nt * 8 + 2 * t + x, tok = u.i * tq + r2 / a.group;
+        const bool on = r2 < tq * a.group && tok < u.s.n_new;
+        limit[nt][x] = on ? u.s.len - u.s.n_new + tok + 1 : 0;
+        qs[nt][x] = a.scale_log2 * __shfl_sync(0xffffffffu, size, (2 * t + x) * 4);
+      }
+    }
+    const int sure = u.s.len - u.s.n_new + u.i * tq + 1;  // keys that every row sees
+
+    float o[NT][STEPS][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int step = 0; step < seg; ++step) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();
+      // the stage of the step before this one, which every lane has left
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);
+      const int key = (u.j + step) * FEW_KEYS + warp * 16;
+      if (key < line.limit(u.s, u.i)) {
+        const uint32_t ks = ring + stage * F::STAGE, vs = ks + 16 * ROW;
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const uint4 lo = lds128(ks + piece<ROW>(g, 4 * i + t));
+          const uint4 hi = lds128(ks + piece<ROW>(g + 8, 4 * i + t));
+          if constexpr (E8) {
+            const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a0 = e4m3_to_half2(w0[x]), a2 = e4m3_to_half2(w0[x] >> 16);
+              const uint32_t a1 = e4m3_to_half2(w1[x]), a3 = e4m3_to_half2(w1[x] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<M>(s[nt], a0, a1, a2, a3, q[nt][4 * i + x][0], q[nt][4 * i + x][1]);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<M>(s[nt], lo.x, hi.x, lo.y, hi.y, q[nt][2 * i][0], q[nt][2 * i][1]);
+              mma16816<M>(s[nt], lo.z, hi.z, lo.w, hi.w, q[nt][2 * i + 1][0],
+                          q[nt][2 * i + 1][1]);
+            }
+          }
+        }
+        // scores of the keys g, g + 8 (index / 2) and the rows 2t, 2t + 1 (index % 2), in
+        // powers of two
+        float kc[2] = {1.f, 1.f}, vl[2] = {0.f, 0.f}, vi[2] = {1.f, 1.f};
+        if constexpr (E8) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            kc[y] = __uint_as_float(lds32(vs + 16 * ROW + (g + 8 * y) * 4));
+            float sv = __uint_as_float(lds32(vs + 16 * ROW + 64 + (g + 8 * y) * 4));
+            sv = sv > 0.f ? sv : 1.f;  // rows left out
+            vl[y] = log2f(sv);
+            vi[y] = 1.0f / sv;
+          }
+        }
+        bool rise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = s[nt][e] * qs[nt][e & 1];
+            if constexpr (E8) x = fmaf(x, kc[e >> 1], vl[e >> 1]);
+            if (key + 16 > sure && key + g + 8 * (e >> 1) >= limit[nt][e & 1]) x = -INFINITY;
+            s[nt][e] = x;
+            rise |= x > m[nt][e & 1] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float top = fmaxf(s[nt][x], s[nt][2 + x]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top = fmaxf(top, m[nt][x]);
+              const float f = top == -INFINITY ? 1.f : ex2(m[nt][x] - top);
+              m[nt][x] = top;
+              l[nt][x] *= f;
+#pragma unroll
+              for (int i = 0; i < STEPS; ++i) {
+                o[nt][i][x] *= f;
+                o[nt][i][2 + x] *= f;
+              }
+            }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float base = m[nt][e & 1];
+            w[e] = ex2(s[nt][e] - (base == -INFINITY ? 0.f : base));
+            l[nt][e & 1] = E8 ? fmaf(w[e], vi[e >> 1], l[nt][e & 1]) : l[nt][e & 1] + w[e];
+          }
+          p[nt][0] = transpose8x8(RowType<M>::pack2(w[0], w[1]));
+          p[nt][1] = transpose8x8(RowType<M>::pack2(w[2], w[3]));
+        }
+        if constexpr (E8) {
+#pragma unroll
+          for (int i = 0; i < STEPS / 2; ++i) {  // 32 dims: dim 32 i + 4 g + x of tile x / 2
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int r = 2 * t + (y & 1) + 8 * (y >> 1);
+              w[y] = lds32(vs + piece<ROW>(r, 2 * i + (g >> 2)) + (g & 3) * 4);
+            }
+            const uint32_t lo01 = __byte_perm(w[0], w[1], 0x5140),
+                           lo23 = __byte_perm(w[0], w[1], 0x7362),
+                           hi01 = __byte_perm(w[2], w[3], 0x5140),
+                           hi23 = __byte_perm(w[2], w[3], 0x7362);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<M>(o[nt][2 * i], e4m3_to_half2(lo01), e4m3_to_half2(lo01 >> 16),
+                          e4m3_to_half2(hi01), e4m3_to_half2(hi01 >> 16), p[nt][0], p[nt][1]);
+              mma16816<M>(o[nt][2 * i + 1], e4m3_to_half2(lo23), e4m3_to_half2(lo23 >> 16),
+                          e4m3_to_half2(hi23), e4m3_to_half2(hi23 >> 16), p[nt][0], p[nt][1]);
+            }
+          }
+        } else {
+          // matrix y = lane / 8: keys 8 (y / 2) .., dims 16 i + 8 (y % 2) ..
+          const int r = (lane & 7) + 8 * (lane >> 4), ch = (lane >> 3) & 1;
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(vs + piece<ROW>(r, 2 * i + ch), v);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<M>(o[nt][i], v[0], v[1], v[2], v[3], p[nt][0], p[nt][1]);
+          }
+        }
+      }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      at.next(line);
+    }
+
+    // ---- join the warps and write the segment
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 4);
+        l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 8);
+        l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 16);
+        const int r = nt * 8 + 2 * t + x;
+        if (g == 0) join_ml[warp * ROWS + r] = make_float2(m[nt][x], l[nt][x]);
+        float* to = join_o + (warp * ROWS + r) * (HD + 4);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          if constexpr (E8) {
+            *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
+                make_float2(o[nt][i][x], o[nt][i][2 + x]);
+          } else {
+            to[16 * i + g] = o[nt][i][x];
+            to[16 * i + 8 + g] = o[nt][i][2 + x];
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = u.j == 0 && seg == u.n;
+    const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
+    for (int x = threadIdx.x; x < ROWS * (HD / 4); x += FEW_THREADS) {
+      const int r = x / (HD / 4), d = x % (HD / 4) * 4, token = u.i * tq + r / a.group;
+      if (r >= tq * a.group || token >= u.s.n_new) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < FEW_WARPS; ++w) top = fmaxf(top, join_ml[w * ROWS + r].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < FEW_WARPS; ++w) {
+        const float2 ml = join_ml[w * ROWS + r];
+        const float f = ex2(ml.x - base);
+        const float4 y = *reinterpret_cast<const float4*>(join_o + (w * ROWS + r) * (HD + 4) + d);
+        sum += f * ml.y;
+        acc.x += f * y.x;
+        acc.y += f * y.y;
+        acc.z += f * y.z;
+        acc.w += f * y.w;
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+        const int head = u.h * a.group + r % a.group;
+        uint2 w;
+        w.x = RowType<T>::pack2(acc.x * inv, acc.y * inv);
+        w.y = RowType<T>::pack2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(a.out + ((long long)(u.s.first + token) * a.o_ts +
+                                           head * a.o_hs + d) * 2) = w;
+        if (a.lse && d == 0)
+          a.lse[(long long)(u.s.first + token) * a.q_heads + head] = row_lse(top, sum);
+      } else {
+        *reinterpret_cast<float4*>(part.o + (slot * ROWS + r) * HD + d) = acc;
+        if (d == 0) part.ml[slot * ROWS + r] = make_float2(top, sum);
+      }
+    }
+    if (u.j == 0 && !whole && threadIdx.x == 0) {
+      Left left = {u.b, u.h, u.i, (u.n - seg + per - 1) / per};
+      part.left[blockIdx.x] = left;
+    }
+    __syncthreads();  // the join buffer is free again
+  }
+  cp_async_wait<0>();
+}
+
+}  // namespace at
+}  // namespace mk

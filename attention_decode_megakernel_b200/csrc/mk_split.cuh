@@ -1,0 +1,278 @@
+// mk_split.cuh -- how an attention call's work is divided over the CTAs, and
+// how partial results are joined.
+//
+// A unit is one tile of query rows of one key head of one sequence: `tq`
+// consecutive new tokens times the `group` query heads that share the head.
+// It walks ceil(limit / KT) tiles of KT keys, where limit is what its last
+// token sees (one tile at least, so that rows without keys are written too).
+// All tiles of all units, ordered by sequence, head, row tile and key tile,
+// form one line, and CTA c takes the tiles [c * per, (c + 1) * per) of it:
+// every CTA gets the same number of key tiles whatever the lengths, for one
+// long sequence as for a ragged batch.  A unit that lies in one CTA's share
+// is finished there.  A unit that crosses shares leaves a partial {sum of
+// weighted values, maximum, sum of weights} in each CTA (a CTA has at most
+// two: slot 2c for the unit it entered in the middle, 2c + 1 for the one it
+// left), and join_kernel adds them in the order of the CTAs: no atomics, the
+// same bits every time, no state kept between calls.
+#pragma once
+#include "mk_attn.cuh"
+
+namespace mk {
+namespace at {
+
+// sum of floor((a i + b) / m) for i < n; a, b >= 0, m > 0 (the Euclid-like
+// recursion on (a, m), a few steps for the sizes here).  U holds a n + b.
+template <class U>
+__device__ __forceinline__ long long floor_sum(U n, U m, U a, U b) {
+  long long s = 0;
+  while (n > 0) {
+    s += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
+    a %= m;
+    b %= m;
+    const U y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const U t = a;
+    a = m;
+    m = t;
+  }
+  return s;
+}
+
+struct Seq {
+  int first, n_new, len;  // first row, new tokens, keys
+};
+
+// Sequence b as the call's device arrays give it, held to the rows and the table.
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s;
+  int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+  lo = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
+  hi = hi < lo ? lo : hi > a.rows ? a.rows : hi;
+  s.first = lo;
+  s.n_new = hi - lo;
+  s.len = s.n_new;
+  if (a.table) {
+    const long long room = (long long)a.table_stride << a.c.page_shift;
+    const int len = a.seq_lens[b];
+    s.len = len < 0 ? 0 : len > room ? int(room) : len;
+  }
+  return s;
+}
+
+template <int KT>
+struct Line {
+  const AttnArgs& a;
+  int tq;
+
+  __device__ int row_tiles(const Seq& s) const { return (s.n_new + tq - 1) / tq; }
+  // keys that the last token of row tile i sees (may be negative)
+  __device__ int limit(const Seq& s, int i) const {
+    const int last = (i + 1) * tq;
+    return s.len - s.n_new + (last < s.n_new ? last : s.n_new);
+  }
+  __device__ int tiles(const Seq& s, int i) const {
+    const int l = limit(s, i);
+    return l <= KT ? 1 : (l + KT - 1) / KT;
+  }
+  // key tiles of the first x row tiles, x < row_tiles: all of them full
+  __device__ long long before(const Seq& s, int x) const {
+    const int past = s.len - s.n_new;
+    // row tiles whose limit is at most 0 count 1
+    const int none = past < 0 ? (-past) / tq : 0;
+    if (none >= x) return x;
+    const long long b = (long long)(none + 1) * tq + past + KT - 1, n = x - none;
+    if (b + n * tq < (1ll << 31))
+      return none + floor_sum<unsigned>(unsigned(n), KT, unsigned(tq), unsigned(b));
+    return none + floor_sum<unsigned long long>(n, KT, tq, b);
+  }
+  // key tiles of one head of the sequence
+  __device__ long long all(const Seq& s) const {
+    const int nq = row_tiles(s);
+    if (nq == 0) return 0;
+    return (nq > 1 ? before(s, nq - 1) : 0) + tiles(s, nq - 1);
+  }
+};
+
+// A place on the line: key tile j of n of row tile i of nq of head h of sequence b.
+template <int KT>
+struct Cursor {
+  Seq s;
+  int b, h, i, j, n, nq;
+  int left;  // tiles of this CTA's share from here on
+
+  __device__ void next(const Line<KT>& line) {
+    --left;
+    if (++j < n || left <= 0) return;
+    j = 0;
+    if (++i == nq) {
+      i = 0;
+      if (++h == line.a.kv_heads) {
+        h = 0;
+        do {  // a tile is left, so a sequence with rows follows
+          s = seq_of(line.a, ++b);
+        } while (s.n_new == 0 && b + 1 < line.a.batch);
+        nq = line.row_tiles(s);
+      }
+    }
+    n = line.tiles(s, i);
+  }
+};
+
+// The place and share of CTA `cta` of `ctas`, shares of at least `least`
+// tiles; `per` receives a share's tiles.  Called by one whole warp with all
+// lanes; the result is the same in every lane.
+template <int KT>
+__device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, int ctas,
+                                                 int least, long long& per) {
+  const AttnArgs& a = line.a;
+  const int lane = threadIdx.x & 31;
+  long long total = 0, mine = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    mine = b < a.batch ? line.all(seq_of(a, b)) * a.kv_heads : 0;
+    long long w = mine;
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    total += w;
+  }
+  per = (total + ctas - 1) / ctas;
+  if (per < least) per = least;
+  Cursor<KT> c = {};
+  const long long at = cta * per;
+  if (at >= total) return c;
+  c.left = int(total - at < per ? total - at : per);
+  // the sequence that holds tile `at`
+  long long before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    if (a.batch > 32) mine = b < a.batch ? line.all(seq_of(a, b)) * a.kv_heads : 0;
+    long long sum = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + sum > at);
+    if (past) {
+      const int found = __ffs(past) - 1;
+      before += __shfl_sync(0xffffffffu, sum - mine, found);
+      c.b = b0 + found;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  c.s = seq_of(a, c.b);
+  c.nq = line.row_tiles(c.s);
+  long long off = at - before;
+  const long long head = line.all(c.s);
+  c.h = int(off / head);
+  off -= c.h * head;
+  // the last row tile that starts at or before `off`: 32 places at a time
+  int lo = 0, span = c.nq;  // it is one of lo .. lo + span - 1
+  while (span > 1) {
+    const int step = (span + 31) / 32, x = lo + lane * step;
+    const bool at_or_before = x == 0 || (lane * step < span && line.before(c.s, x) <= off);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, at_or_before));
+    span = span - last * step < step ? span - last * step : step;
+    lo += last * step;
+  }
+  c.i = lo;
+  c.j = int(off - (lo ? line.before(c.s, lo) : 0));
+  c.n = line.tiles(c.s, c.i);
+  return c;
+}
+
+// Partial results in the workspace: for slot s the rows' weighted sums
+// [R][HD], their {maximum, sum} [R], and for each CTA the unit that it left unfinished.
+struct Left {
+  int b, h, i;
+  int more;  // CTAs behind this one that hold the rest; 0: nothing was left
+};
+struct Partials {
+  float* o;
+  float2* ml;
+  Left* left;
+};
+inline __host__ __device__ size_t partial_bytes(int ctas, int rows, int hd) {
+  return size_t(ctas) * (2 * size_t(rows) * (hd + 2) * 4 + sizeof(Left));
+}
+inline __host__ Partials carve(void* ws, int ctas, int rows, int hd) {
+  Partials p;
+  p.o = static_cast<float*>(ws);
+  p.ml = reinterpret_cast<float2*>(p.o + size_t(2) * ctas * rows * hd);
+  p.left = reinterpret_cast<Left*>(p.ml + size_t(2) * ctas * rows);
+  return p;
+}
+
+// The natural logarithm of a row's sum of weights 2^x = l * 2^m.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : l == 0.f ? -INFINITY : l;
+}
+
+// Joins the partials of the unit that CTA blockIdx.x left unfinished: block
+// (c, y) takes the rows y * ROWS .. of it, a warp for each row; the lanes
+// hold the row's values, the partials are read in the CTAs' order.
+constexpr int JOIN_ROWS = 4;
+template <class T, int HD>
+__global__ void __launch_bounds__(JOIN_ROWS * 32)
+    join_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows, int tq) {
+  griddep_wait();
+  const Left u = p.left[blockIdx.x];
+  if (u.more <= 0) return;
+  const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const Seq s = seq_of(a, u.b);
+  const int first = s.first, token = u.i * tq + r / a.group;
+  if (r >= tq * a.group || token >= s.n_new) return;
+  constexpr int N = HD / 32;  // values of a lane, in pieces of 4 (2 for HD 64)
+  constexpr int V = N < 4 ? N : 4;
+  float m = -INFINITY;
+  for (int k = lane; k <= u.more; k += 32) {
+    const size_t slot = k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
+    m = fmaxf(m, p.ml[slot * rows + r].x);
+  }
+  m = warp_max(m);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = 0.f;
+#pragma unroll 8
+  for (int k = 0; k <= u.more; ++k) {
+    const size_t slot = k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
+    const float2 ml = p.ml[slot * rows + r];
+    const float f = exp2f(ml.x - base);
+    l += f * ml.y;
+    const float* src = p.o + (slot * rows + r) * HD + lane * V;
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src + i * 32);
+        o[i] += f * x.x;
+        o[i + 1] += f * x.y;
+        o[i + 2] += f * x.z;
+        o[i + 3] += f * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        o[0] += f * x.x;
+        o[1] += f * x.y;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int head = u.h * a.group + r % a.group;
+  unsigned char* out = a.out + ((long long)(first + token) * a.o_ts + head * a.o_hs + lane * V) * 2;
+#pragma unroll
+  for (int i = 0; i < N; i += V) {
+    if constexpr (V == 4) {
+      uint2 w;
+      w.x = RowType<T>::pack2(o[i] * inv, o[i + 1] * inv);
+      w.y = RowType<T>::pack2(o[i + 2] * inv, o[i + 3] * inv);
+      *reinterpret_cast<uint2*>(out + i * 64) = w;
+    } else {
+      *reinterpret_cast<uint32_t*>(out) = RowType<T>::pack2(o[0] * inv, o[1] * inv);
+    }
+  }
+  if (a.lse && lane == 0) a.lse[(long long)(first + token) * a.q_heads + head] = row_lse(m, l);
+}
+
+}  // namespace at
+}  // namespace mk
