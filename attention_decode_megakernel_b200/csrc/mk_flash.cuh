@@ -1,0 +1,779 @@
+// mk_flash.cuh -- attention of many query rows on the tensor cores: whole
+// packed prompts, and chunks of new tokens over a paged cache.
+//
+// A unit's rows (tokens times the heads of the group) are tiles of 128, the M
+// of tcgen05.mma; keys come in tiles of 128. For head_dim 64 and 128 two row
+// tiles share every key tile (two streams, 256 rows); at 256 the output alone
+// takes half of tensor memory and one row tile has two score buffers.
+//
+//   S = Q K^T   both from shared memory, 128 x 128 fp32 into TMEM
+//   P = 2^(S c - m)  by a warpgroup, a thread for each row: scores from TMEM,
+//                    weights back as 16-bit pairs over the scores' columns
+//   O += P V    P from TMEM, V as it lies in memory (MN-major)
+//
+// Warps: one TMA producer, one MMA issuer, a softmax warpgroup for each
+// stream (one at head_dim 256).  While a warpgroup works on one tile, the
+// tensor cores run the other stream's products (or the next tile's scores and
+// the last one's output).  The maximum of a row is raised only when a score
+// passes it by far (mk_paged.cuh, Weights), and only then is O rescaled in TMEM;
+// the sum of weights is kept in fp32 from the unrounded weights.
+//
+// K and V tiles: one TMA box of 64 dims by min(page, 128) positions each, the
+// page looked up by the producer's lanes; boxes behind the last key and of
+// pages outside the cache lie outside the tensor and arrive as zeros.  What the
+// last page holds behind the sequence is zeroed in V before it is used (its
+// scores are masked, but 0 * NaN is NaN).  An e4m3 cache has a warpgroup
+// of converters in the producer's place: codes through registers to fp16
+// tiles, exactly, the rows' scales beside them; queries become fp16 after a
+// power of two for each row.
+//
+// Every wait is bounded; one that runs out makes the CTA write NaN.
+#pragma once
+#include "mk_paged.cuh"
+#include "mk_tc.cuh"
+
+namespace mk {
+namespace at {
+
+constexpr int KEYS = 128;  // keys of a tile
+constexpr long long FLASH_WAIT_NS = 2000000000LL;
+
+template <class C, int HD>
+struct FlashCfg {
+  static constexpr bool E8 = __is_same(C, E4m3);
+  static constexpr int NQ = HD == 256 ? 1 : 2;  // row tiles (streams)
+  static constexpr int CHUNKS = HD / 64;        // 64-value columns of an operand
+  static constexpr int PARTS = HD == 256 ? 2 : 1;  // ring stages of a K or V tile
+  static constexpr int VK = KEYS / PARTS;          // keys of a V stage
+  static constexpr int KC = CHUNKS / PARTS;        // 64-value columns of a K stage
+  static constexpr int STAGE = KEYS * KC * 128;    // bytes
+  static constexpr int Q_TILE = 128 * HD * 2;
+  static constexpr int STAGES = HD == 64 ? 8 : E8 ? 4 : 5;
+  static constexpr int SCALES = E8 ? 8 : 0;  // tiles whose scales are kept
+  static constexpr int SOFT_WARPS = 4 * NQ;
+  static constexpr int THREADS = 128 + SOFT_WARPS * 32 + (E8 ? 128 : 0);
+  static constexpr size_t SMEM = 1024 + size_t(NQ) * Q_TILE + size_t(STAGES) * STAGE +
+                                 size_t(SCALES) * 3 * KEYS * 4 + (E8 ? 2 * NQ * 128 * 4 : 0);
+  // registers of a thread: launched with, softmax, the others
+  static constexpr int REGS_SOFT = THREADS == 512 ? 200 : THREADS == 384 ? (NQ == 2 ? 216 : 232) : 0;
+  static constexpr int REGS_REST = THREADS == 512 ? 56 : THREADS == 384 ? (NQ == 2 ? 72 : 136) : 0;
+  static_assert(REGS_SOFT * SOFT_WARPS * 32 + REGS_REST * (THREADS - SOFT_WARPS * 32) <=
+                    (65536 / THREADS / 8 * 8) * THREADS,
+                "the shares exceed what the block is launched with");
+};
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  if constexpr (N > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  if constexpr (N > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct FlashArgs {
+  AttnArgs a;
+  CUtensorMap q, k, v;  // q: (dim, head of the group, row, key head); k, v: (dim, position, head, page)
+  int tq1;              // tokens of a row tile
+  int box_shift;        // log2 of the positions of a K box
+  int least;
+};
+
+struct FlashBars {
+  uint64_t q_full, q_ready, q_empty;
+  uint64_t full[8], empty[8];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t sc_full[8];
+  uint32_t tmem;
+  int gave_up;
+  int per;
+  Cursor<KEYS> start;
+};
+
+__device__ __forceinline__ bool flash_wait(uint64_t* bar, uint32_t parity, FlashBars* f) {
+  uint64_t start = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t now = global_ns();
+    if (start == 0) start = now;
+    if (now - start > uint64_t(FLASH_WAIT_NS) || *(volatile int*)&f->gave_up) {
+      *(volatile int*)&f->gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a warp whose first lane works between the waits: the others
+// stay with it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, FlashBars* f) {
+  __syncwarp();
+  return flash_wait(bar, parity, f);
+}
+
+// {x0, x1} * {y, y} + {c, c}
+__device__ __forceinline__ void fma2(float& x0, float& x1, float y, float c) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%2, %2};\n\t"
+      "mov.b64 d, {%3, %3};\n\t"
+      "fma.rn.f32x2 a, a, b, d;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x0, float x1) {
+  asm("{\n\t.reg .b64 c, x;\n\t"
+      "mov.b64 c, {%0, %1};\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "add.rn.f32x2 c, c, x;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x0), "f"(x1));
+}
+
+template <class T, class C, int HD, bool PAGED>
+__global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
+    flash_kernel(const __grid_constant__ FlashArgs fa, Partials part) {
+  using F = FlashCfg<C, HD>;
+  constexpr bool E8 = F::E8, BF = !E8 && __is_same(T, Bf16);
+  constexpr bool RESCALE_Q = E8 && __is_same(T, Bf16);
+  constexpr int NQ = F::NQ, STAGES = F::STAGES, PARTS = F::PARTS, CHUNKS = F::CHUNKS;
+  using M = typename std::conditional<E8, Fp16, T>::type;
+  const AttnArgs& a = fa.a;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ FlashBars f;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  unsigned char* base_ptr = smem_raw + (base - smem_addr(smem_raw));
+  const uint32_t sq = base, ring = base + NQ * F::Q_TILE;
+  float* scales = reinterpret_cast<float*>(base_ptr + NQ * F::Q_TILE + STAGES * F::STAGE);
+  float* q_size = scales + F::SCALES * 3 * KEYS;  // [2][NQ * 128]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Line<KEYS> line{a, NQ * fa.tq1};
+  const int tq1 = fa.tq1, tile_rows = tq1 * a.group;
+
+  if (warp == 0) {
+    long long per;
+    const Cursor<KEYS> c = find_share<KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
+    if (lane == 0) {
+      f.per = int(per);
+      f.start = c;
+      f.gave_up = 0;
+      Left none = {0, 0, 0, 0};
+      part.left[blockIdx.x] = none;
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&f.tmem, 512);
+  } else if (warp == 2 && lane == 0) {
+    mbar_init(&f.q_full, 1);
+    mbar_init(&f.q_ready, 4);
+    mbar_init(&f.q_empty, 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&f.full[i], E8 ? 4 : 1);
+      mbar_init(&f.empty[i], 1);
+      mbar_init(&f.sc_full[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&f.s_full[i], 1);
+      mbar_init(&f.p_full[i], 4);
+      mbar_init(&f.o_full[i], 1);
+      mbar_init(&f.o_empty[i], 4);
+    }
+    fence_barrier_init();
+  } else if (warp == 3 && lane == 0) {
+    prefetch_map(&fa.q);
+    if (!E8) {
+      prefetch_map(&fa.k);
+      prefetch_map(&fa.v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = f.tmem;
+  Cursor<KEYS> at = f.start;
+
+  // streams of a unit: the second row tile may have no tokens
+  auto streams = [&](const Cursor<KEYS>& u) {
+    return NQ == 2 && u.s.n_new - u.i * NQ * tq1 > tq1 ? 2 : 1;
+  };
+  // end of stream s's key tiles within a segment that ends at tile `end`
+  auto stream_end = [&](const Cursor<KEYS>& u, int s, int end) {
+    if (NQ == 1 || s == 1) return end;
+    const int last = u.i * NQ * tq1 + tq1;
+    const int limit = u.s.len - u.s.n_new + (last < u.s.n_new ? last : u.s.n_new);
+    const int n = limit <= KEYS ? 1 : (limit + KEYS - 1) / KEYS;
+    return n < end ? n : end;
+  };
+
+  // Each warpgroup changes its registers inside its own branch: code after a
+  // common point would be held to the smallest share.
+  if (warp < 4) {
+    fewer_registers<F::REGS_REST>();
+  if (warp == 0) {
+    // ---- TMA producer: queries, and keys and values unless they are converted
+    int it = 0, seg_no = 0, issued = 0;
+    while (at.left > 0 && !f.gave_up) {
+      const int seg = at.segment(), ns = streams(at);
+      bool ok = seg_no == 0 || warp_wait(&f.q_empty, (seg_no - 1) & 1, &f);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
+      __syncwarp();
+      if (lane < ns * CHUNKS) {
+        const int s = lane / CHUNKS, c = lane % CHUNKS;
+        tma_load_4d(sq + s * F::Q_TILE + c * (128 * 128), &fa.q, c * 64, 0,
+                    at.s.first + at.i * NQ * tq1 + s * tq1, at.h, &f.q_full);
+      }
+      if constexpr (!E8) {
+        const int limit = line.limit(at.s, at.i), end = at.j + seg;
+        const int shift = PAGED ? fa.box_shift : 7;
+        // lane b: the page of box b of the tile, looked up a tile ahead
+        auto pages_of = [&](int j) {
+          int page = a.c.n_pages;
+          if constexpr (PAGED) {
+            const int key = j * KEYS + (lane << shift);
+            if ((lane << shift) < KEYS && key < limit) {
+              page = a.table[(long long)at.b * a.table_stride + (key >> a.c.page_shift)];
+              if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;
+            }
+          }
+          return page;
+        };
+        auto load = [&](bool v, int j, int pages) {
+          for (int p = 0; p < PARTS; ++p, ++it) {
+            const int st = it % STAGES;
+            if (it >= STAGES && !warp_wait(&f.empty[st], (it / STAGES - 1) & 1, &f)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&f.full[st], F::STAGE);
+            __syncwarp();
+            issued = it + 1;
+            const int rows = v && F::VK < (1 << shift) ? F::VK : 1 << shift;  // of a box
+            const int per_col = (v ? F::VK : KEYS) / rows, cols = v ? CHUNKS : F::KC;
+            for (int x0 = 0; x0 < per_col * cols; x0 += 32) {
+              const int x = x0 + lane, c = x / per_col, b = x % per_col;
+              const int row = b * rows;                     // in the stage
+              const int key = row + (v ? p * F::VK : 0);    // in the tile
+              const int page = __shfl_sync(0xffffffffu, pages, (key >> shift) & 31);
+              if (x < per_col * cols) {
+                const uint32_t dst =
+                    ring + st * F::STAGE + (c * (v ? F::VK : KEYS) + row) * 128;
+                const int dim = (c + (v ? 0 : p * F::KC)) * 64;
+                const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
+                                      : at.s.first + j * KEYS + key;
+                tma_load_4d(dst, v ? &fa.v : &fa.k, dim, pos, at.h, PAGED ? page : 0,
+                            &f.full[st]);
+              }
+            }
+          }
+          return true;
+        };
+        int now = pages_of(at.j), next = pages_of(at.j + 1 < end ? at.j + 1 : at.j);
+        ok = load(false, at.j, now);
+        for (int j = at.j; ok && j < end; ++j) {
+          if (NQ == 1) {  // scores run a tile ahead of the output
+            if (j + 1 < end) ok = load(false, j + 1, next);
+            ok = ok && load(true, j, now);
+          } else {
+            ok = load(true, j, now);
+            if (j + 1 < end) ok = ok && load(false, j + 1, next);
+          }
+          now = next;
+          next = pages_of(j + 2 < end ? j + 2 : at.j);
+        }
+        if (!ok) break;
+      }
+      at.skip(line, seg);
+      ++seg_no;
+    }
+    // copies in flight must land before the CTA can end
+    if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f);
+    if (!E8)
+      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) {
+        const uint64_t start = global_ns();
+        while (!mbar_try_wait(&f.full[i % STAGES], (i / STAGES) & 1))
+          if (global_ns() - start > uint64_t(FLASH_WAIT_NS)) break;
+      }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    constexpr uint32_t id_s = idesc_f16(BF, 128, KEYS, false), id_o = idesc_f16(BF, 128, HD, true);
+    int it = 0, seg_no = 0;
+    int cnt[2] = {0, 0};   // key tiles of a stream so far
+    int segs[2] = {0, 0};  // its segments so far: each ends with an epilogue that reads O
+    bool ok = true;
+    auto issue_s = [&](int slot, int q, int at_it) {
+      uint64_t qd = desc_k_major(sq + q * F::Q_TILE);
+#pragma unroll 1
+      for (int c = 0; c < CHUNKS; ++c, qd += 128 * 128 / 16) {
+        const int st = (at_it + c / F::KC) % STAGES;
+        const uint64_t kd = desc_k_major(ring + st * F::STAGE + (c % F::KC) * (KEYS * 128));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, c + k > 0);
+      }
+    };
+    auto issue_o = [&](int slot, int s, int at_it, bool more) {
+#pragma unroll 1
+      for (int p = 0; p < PARTS; ++p) {
+        const int st = (at_it + p) % STAGES;
+        const uint64_t vd = desc_mn_major(ring + st * F::STAGE, F::VK * 128);
+#pragma unroll 4
+        for (int k = 0; k < F::VK / 16; ++k)
+          tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + (p * F::VK + k * 16) / 2,
+                    vd + k * (2048 / 16), id_o, more || p + k > 0);
+      }
+    };
+    auto wait_parts = [&](int at_it) {
+      for (int p = 0; p < PARTS; ++p)
+        if (!warp_wait(&f.full[(at_it + p) % STAGES], ((at_it + p) / STAGES) & 1, &f))
+          return false;
+      return true;
+    };
+    auto release = [&](int at_it) {
+      for (int p = 0; p < PARTS; ++p) tc_commit(&f.empty[(at_it + p) % STAGES]);
+    };
+    // zero what lies behind the sequence in the V tile of stages at_it ..
+    auto clear_tail = [&](int at_it, int j, int len) {
+      if constexpr (!E8) {
+        if (len >= (j + 1) * KEYS) return;
+        for (int p = 0; p < PARTS; ++p) {
+          const int keep = len - j * KEYS - p * F::VK;
+          for (int x = lane; x < F::VK * 8; x += 32) {
+            if (x / 8 < keep) continue;
+            const uint32_t to = ring + ((at_it + p) % STAGES) * F::STAGE + x * 16;
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + c * F::VK * 128),
+                           "r"(0)
+                           : "memory");
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+      }
+    };
+    while (at.left > 0 && ok) {
+      const int seg = at.segment(), end = at.j + seg, ns = streams(at);
+      ok = warp_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f);
+      if (!ok) break;
+      int e[2] = {stream_end(at, 0, end), ns == 2 ? end : at.j};
+      bool first[2] = {true, true};
+      // O is free once the epilogue of the stream's last segment has read it
+      auto wait_o = [&](int s) {
+        return segs[s] == 0 || warp_wait(&f.o_empty[s], (segs[s] - 1) & 1, &f);
+      };
+      int k_it = it, v_it;
+      it += PARTS;
+      ok = wait_parts(k_it);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        for (int s = 0; s < NQ; ++s)
+          if (at.j < e[s]) {
+            const int slot = NQ == 1 ? cnt[0] & 1 : s;
+            issue_s(slot, s, k_it);
+            tc_commit(&f.s_full[slot]);
+          }
+        release(k_it);
+        if (seg == 1) tc_commit(&f.q_empty);
+      }
+      for (int j = at.j; j < end && ok; ++j) {
+        const bool more = j + 1 < end;
+        bool have_k = false;
+        if (NQ == 1 && more) {
+          // the next tile's scores before this tile's output
+          k_it = it;
+          it += PARTS;
+          ok = wait_parts(k_it);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const int slot = (cnt[0] + 1) & 1;
+            issue_s(slot, 0, k_it);
+            tc_commit(&f.s_full[slot]);
+            release(k_it);
+            if (j + 2 == end) tc_commit(&f.q_empty);
+          }
+        }
+        v_it = it;
+        it += PARTS;
+        if (NQ == 2 && more) {
+          k_it = it;
+          it += PARTS;
+        }
+        ok = wait_parts(v_it);
+        if (!ok) break;
+        clear_tail(v_it, j, at.s.len);
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+          if (j >= e[s]) continue;
+          const int slot = NQ == 1 ? cnt[0] & 1 : s;
+          if (first[s]) ok = wait_o(s);
+          ok = ok && warp_wait(&f.p_full[slot], (NQ == 1 ? cnt[0] >> 1 : cnt[s]) & 1, &f);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            issue_o(slot, s, v_it, !first[s]);
+            tc_commit(&f.o_full[slot]);
+          }
+          first[s] = false;
+          ++cnt[s];
+          if (NQ == 2 && j + 1 < e[s]) {
+            if (!have_k) {
+              ok = wait_parts(k_it);
+              if (!ok) break;
+              tc_fence_after();
+              have_k = true;
+            }
+            if (lane == 0) {
+              issue_s(s, s, k_it);
+              tc_commit(&f.s_full[s]);
+            }
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          release(v_it);
+          if (NQ == 2 && more) release(k_it);
+          if (NQ == 2 && j + 2 == end) tc_commit(&f.q_empty);
+        }
+      }
+      for (int s = 0; s < ns && ok; ++s) {
+        if (first[s]) ok = wait_o(s);  // a stream without tiles here: keep step with its epilogues
+        ++segs[s];
+      }
+      at.skip(line, seg);
+      ++seg_no;
+    }
+    __syncwarp();
+  }
+  } else if (warp < 4 + F::SOFT_WARPS) {
+    // ---- softmax and epilogue: a thread for each row of stream s
+    more_registers<F::REGS_SOFT>();
+    const int s = (warp - 4) >> 2, r = tid & 127, quarter = warp & 3;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    int cnt = 0, seg_no = 0, tiles = 0;  // own key tiles, segments, all key tiles so far
+    // The output through key tile x.  Its barrier goes by the score buffer: with one
+    // stream the scores of tile x + 1 come before the output of tile x, so that two
+    // outputs may be due at once, and one barrier's parity could not tell them apart.
+    auto wait_output = [&](int x) {
+      return flash_wait(&f.o_full[NQ == 1 ? x & 1 : s], (NQ == 1 ? x >> 1 : x) & 1, &f);
+    };
+    while (at.left > 0) {
+      const Cursor<KEYS> u = at;
+      const int seg = u.segment(), end = u.j + seg;
+      at.skip(line, seg);
+      const int parity_seg = seg_no++, tile0 = tiles - u.j;
+      tiles += seg;
+      if (s >= streams(u)) continue;
+      const int e = stream_end(u, s, end);
+      const int token = (u.i * NQ + s) * tq1 + r / a.group;
+      const bool live = r < tile_rows && token < u.s.n_new;
+      const int limit = live ? u.s.len - u.s.n_new + token + 1 : 0;
+      const int sure = u.s.len - u.s.n_new + (u.i * NQ + s) * tq1 + 1;  // every row sees so many
+      const bool any_live = __any_sync(0xffffffffu, live);
+      float m = -INFINITY, l0 = 0.f, l1 = 0.f;  // m in powers of two
+      float c = a.scale_log2;
+      bool ok = true;
+      for (int j = u.j; j < e && ok; ++j, ++cnt) {
+        const int slot = NQ == 1 ? cnt & 1 : s;
+        const uint32_t scores = lanes + slot * KEYS;
+        const float* sc = scales + ((tile0 + j) & 7) * 3 * KEYS;
+        ok = flash_wait(&f.s_full[slot], (NQ == 1 ? cnt >> 1 : cnt) & 1, &f);
+        if constexpr (E8) ok = ok && flash_wait(&f.sc_full[(tile0 + j) & 7], (tile0 + j) >> 3 & 1, &f);
+        // (the converters wrote it before the first tile's scales)
+        if (RESCALE_Q && j == u.j)
+          c = a.scale_log2 * q_size[(parity_seg & 1) * NQ * 128 + s * 128 + r];
+        if (!ok) break;
+        tc_fence_after();
+        if (any_live) {
+          float x[KEYS];
+#pragma unroll
+          for (int i = 0; i < KEYS; i += 32) tmem_ld32(scores + i, x + i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < KEYS; ++i) pin(x[i]);
+          if constexpr (E8) {
+#pragma unroll
+            for (int i = 0; i < KEYS; i += 4) {
+              const float4 kc = *reinterpret_cast<const float4*>(sc + i);
+              const float4 vl = *reinterpret_cast<const float4*>(sc + KEYS + i);
+              x[i] = fmaf(x[i] * c, kc.x, vl.x);
+              x[i + 1] = fmaf(x[i + 1] * c, kc.y, vl.y);
+              x[i + 2] = fmaf(x[i + 2] * c, kc.z, vl.z);
+              x[i + 3] = fmaf(x[i + 3] * c, kc.w, vl.w);
+            }
+          }
+          if (j * KEYS + KEYS > sure) {
+            const int keep = limit - j * KEYS;
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) x[i] = i < keep ? x[i] : -INFINITY;
+          }
+          float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+#pragma unroll
+          for (int i = 4; i < KEYS; i += 4) {
+            t0 = fmaxf(t0, x[i]);
+            t1 = fmaxf(t1, x[i + 1]);
+            t2 = fmaxf(t2, x[i + 2]);
+            t3 = fmaxf(t3, x[i + 3]);
+          }
+          const float unit = E8 ? 1.f : c;
+          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * unit;
+          const bool rise = top > m + Weights<M>::RAISE;
+          if (__any_sync(0xffffffffu, rise)) {
+            const float up = rise ? top - Weights<M>::LIFT : m;
+            const float fac = rise ? ex2(m - up) : 1.f;
+            l0 *= fac;
+            l1 *= fac;
+            m = up;
+            if (j > u.j) {
+              // the last tile's output is complete; scale it
+              ok = wait_output(cnt - 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < HD; d += 32) {
+                float o[32];
+                tmem_ld32(lanes + 256 + s * HD + d, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  pin(o[i]);
+                  o[i] *= fac;
+                }
+                tmem_st32(lanes + 256 + s * HD + d, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : -m;
+          const float* vi = sc + 2 * KEYS;
+#pragma unroll
+          for (int i = 0; i < KEYS; i += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              float &p0 = x[i + y], &p1 = x[i + y + 1];
+              fma2(p0, p1, unit, off);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              if constexpr (E8) {
+                const float2 w = *reinterpret_cast<const float2*>(vi + i + y);
+                l0 = fmaf(p0, w.x, l0);
+                l1 = fmaf(p1, w.y, l1);
+              } else {
+                add2(l0, l1, p0, p1);
+              }
+              p[y / 2] = RowType<M>::pack2(p0, p1);
+            }
+            tmem_st16(scores + i / 2, p);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&f.p_full[slot]);
+      }
+      // ---- epilogue
+      if (ok && e > u.j) ok = wait_output(cnt - 1);
+      tc_fence_after();
+      const bool whole = u.j == 0 && seg == u.n;
+      float l = l0 + l1;
+      if (!ok) l = m = __int_as_float(0x7FC00000);  // a wait ran out: NaN
+      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+      const int head = u.h * a.group + r % a.group;
+      const long long row = u.s.first + (live ? token : 0);
+      const size_t slot_row =
+          (2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0)) * (NQ * 128) + s * tile_rows + r;
+      if (any_live) {
+#pragma unroll 1
+        for (int d = 0; d < HD; d += 32) {
+          float o[32];
+          tmem_ld32(lanes + 256 + s * HD + d, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            pin(o[i]);
+            o[i] = e > u.j ? o[i] * inv : 0.f;
+            if (!ok) o[i] = l;
+          }
+          if (live && whole) {
+            uint4* to = reinterpret_cast<uint4*>(a.out + (row * a.o_ts + head * a.o_hs + d) * 2);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              to[i / 8] = make_uint4(
+                  RowType<T>::pack2(o[i], o[i + 1]), RowType<T>::pack2(o[i + 2], o[i + 3]),
+                  RowType<T>::pack2(o[i + 4], o[i + 5]), RowType<T>::pack2(o[i + 6], o[i + 7]));
+          } else if (live) {
+            float4* to = reinterpret_cast<float4*>(part.o + slot_row * HD + d);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              to[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (live && whole) {
+          if (a.lse) a.lse[row * a.q_heads + head] = row_lse(m, l);
+        } else if (live) {
+          part.ml[slot_row] = make_float2(m, l);
+        }
+      }
+      if (s == 0 && r == 0 && u.j == 0 && !whole) {
+        Left left = {u.b, u.h, u.i, (u.n - seg + f.per - 1) / f.per};
+        part.left[blockIdx.x] = left;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&f.o_empty[s]);
+    }
+  } else if constexpr (E8) {
+    // ---- converters of an e4m3 cache (and of bf16 queries that meet it)
+    fewer_registers<F::REGS_REST>();
+    const int ct = tid - 128 - F::SOFT_WARPS * 32;
+    constexpr int N = F::STAGE / 32 / 128;  // 16-code pieces of a thread and stage
+    int it = 0, seg_no = 0, tiles = 0;
+    while (at.left > 0 && !*(volatile int*)&f.gave_up) {
+      const int seg = at.segment(), end = at.j + seg, ns = streams(at);
+      bool ok = true;
+      if constexpr (RESCALE_Q) {
+        ok = flash_wait(&f.q_full, seg_no & 1, &f);
+        if (!ok) break;
+        for (int s = 0; s < ns; ++s) {
+          const uint32_t row = sq + s * F::Q_TILE + ct * 128;
+          float size = 0.f;
+#pragma unroll 4
+          for (int x = 0; x < CHUNKS * 8; ++x) {  // the lanes' pieces turned: no bank conflicts
+            const uint4 w = lds128(row + (x >> 3) * (128 * 128) + (((x + ct) & 7) << 4));
+            float v[8];
+            RowType<Bf16>::unpack(w, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) size = fmaxf(size, fabsf(v[i]));
+          }
+          uint32_t ex = __float_as_uint(size) >> 23;
+          ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
+          const float down = __uint_as_float((254 - ex) << 23);
+          q_size[(seg_no & 1) * NQ * 128 + s * 128 + ct] = __uint_as_float(ex << 23);
+#pragma unroll 4
+          for (int x = 0; x < CHUNKS * 8; ++x) {
+            const uint32_t p = row + (x >> 3) * (128 * 128) + (((x + ct) & 7) << 4);
+            const uint4 w = lds128(p);
+            float v[8];
+            RowType<Bf16>::unpack(w, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= down;
+            const uint4 h = RowType<Fp16>::pack(v);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(h.x), "r"(h.y),
+                         "r"(h.z), "r"(h.w)
+                         : "memory");
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&f.q_ready);
+      }
+      // stage n of the segment in the order in which the issuer takes them
+      const int len = at.s.len, j0 = at.j;
+      auto what = [&](int n, bool& v, int& j, int& p) {
+        const int x = n / PARTS;
+        p = n % PARTS;
+        if (NQ == 2) {
+          v = x & 1;
+          j = j0 + (x >> 1);
+        } else if (x & 1) {
+          v = (x + 1) / 2 >= seg;
+          j = v ? end - 1 : j0 + (x + 1) / 2;
+        } else {
+          v = x > 0;
+          j = x > 0 ? j0 + x / 2 - 1 : j0;
+        }
+      };
+      auto place = [&](int x, bool v, int& row, int& pc) {
+        const int per = v ? CHUNKS * 4 : F::KC * 4;
+        row = x / per;
+        pc = x % per;
+      };
+      auto page_of = [&](int key) {
+        const int page = key < len ? __ldg(a.table + (long long)at.b * a.table_stride +
+                                           (key >> a.c.page_shift))
+                                   : -1;
+        return page < a.c.n_pages ? page : -1;
+      };
+      auto load = [&](int n, uint4 (&w)[N]) {
+        bool v;
+        int j, p;
+        what(n, v, j, p);
+        const unsigned char* src = v ? a.c.v : a.c.k;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          int row, pc;
+          place(i * 128 + ct, v, row, pc);
+          const int key = j * KEYS + (v ? p * F::VK : 0) + row;
+          const int page = page_of(key);
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (page >= 0)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(
+                src + page * a.c.page_stride + at.h * a.c.head_stride +
+                (key & (a.c.page_size - 1)) * a.c.pos_stride + (v ? 0 : p * F::KC * 64) + pc * 16));
+        }
+      };
+      uint4 cur[N], next[N];
+      load(0, cur);
+      for (int n = 0; n < 2 * seg * PARTS; ++n, ++it) {
+        bool v;
+        int j, p;
+        what(n, v, j, p);
+        float ks = 0.f, vs = 1.f;
+        const bool first = !v && p == 0;
+        if (first) {
+          const int key = j * KEYS + ct, page = page_of(key);
+          if (page >= 0) {
+            const long long at_scale =
+                (((long long)page * a.c.kv_heads + at.h) << a.c.page_shift) +
+                (key & (a.c.page_size - 1));
+            ks = __ldg(a.c.k_scale + at_scale);
+            vs = __ldg(a.c.v_scale + at_scale);
+          }
+        }
+        if (n + 1 < 2 * seg * PARTS) load(n + 1, next);
+        const int st = it % STAGES;
+        ok = it < STAGES || flash_wait(&f.empty[st], (it / STAGES - 1) & 1, &f);
+        if (!ok) break;
+        const int rows = v ? F::VK : KEYS;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          int row, pc;
+          place(i * 128 + ct, v, row, pc);
+          const uint32_t to = ring + st * F::STAGE + ((pc >> 2) * rows + row) * 128;
+          const uint32_t x = (pc & 3) * 2, turn = row & 7;
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + ((x ^ turn) << 4)),
+                       "r"(e4m3_to_half2(cur[i].x)), "r"(e4m3_to_half2(cur[i].x >> 16)),
+                       "r"(e4m3_to_half2(cur[i].y)), "r"(e4m3_to_half2(cur[i].y >> 16))
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + (((x + 1) ^ turn) << 4)),
+                       "r"(e4m3_to_half2(cur[i].z)), "r"(e4m3_to_half2(cur[i].z >> 16)),
+                       "r"(e4m3_to_half2(cur[i].w)), "r"(e4m3_to_half2(cur[i].w >> 16))
+                       : "memory");
+        }
+        if (first) {
+          const int slot = (tiles + j - j0) & 7;
+          float* to = scales + slot * 3 * KEYS + ct;
+          to[0] = ks;
+          to[KEYS] = log2f(vs);
+          to[2 * KEYS] = 1.0f / vs;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&f.sc_full[slot]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&f.full[st]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) cur[i] = next[i];
+      }
+      if (!ok) break;
+      tiles += seg;
+      at.skip(line, seg);
+      ++seg_no;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace at
+}  // namespace mk

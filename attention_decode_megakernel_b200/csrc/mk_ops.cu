@@ -7,6 +7,7 @@
 
 #include "mk.h"
 #include "mk_attn.cuh"
+#include "mk_flash.cuh"
 #include "mk_kvcache.cuh"
 #include "mk_paged.cuh"
 #include "mk_rope.cuh"
@@ -289,6 +290,7 @@ int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, vo
     return MK_ERR_ARG;
   if (!head_dim_ok(head_dim)) return MK_ERR_UNSUPPORTED;
   if (q_heads % kv_heads) return MK_ERR_ARG;
+  if (q_heads / kv_heads > 128) return MK_ERR_UNSUPPORTED;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return MK_ERR_ARG;
   if (rows == 0 || batch == 0) return MK_OK;
   if (!rows_ok(q, q_ts, q_hs, 2) || !rows_ok(out, o_ts, o_hs, 2) || !cu_q || !aligned(cu_q, 4) ||
@@ -373,6 +375,93 @@ int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream
   return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, F::ROWS, tq, st);
 }
 
+// cuTensorMapEncodeTiled through the runtime (no link against the driver library).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_tiled() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// A 4D view of 16-bit values, strides in values for the dims 1 .. 3, boxes of
+// 64 values by b1 by b2, in the 128-byte swizzle; outside the view reads as zero.
+bool encode_map(CUtensorMap* m, const void* base, bool bf16, long long d0, long long d1,
+                long long d2, long long d3, long long s1, long long s2, long long s3, int b1,
+                int b2) {
+  const EncodeFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2), cuuint64_t(d3)};
+  // the stride of a dim of one is never walked; zero is not a valid one
+  const cuuint64_t strides[3] = {s1 > 0 ? cuuint64_t(s1) * 2 : 16, s2 > 0 ? cuuint64_t(s2) * 2 : 16,
+                                 s3 > 0 ? cuuint64_t(s3) * 2 : 16};
+  const cuuint32_t box[4] = {64u, cuuint32_t(b1), cuuint32_t(b2), 1u}, step[4] = {1u, 1u, 1u, 1u};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, class C, int HD, bool PAGED>
+int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+  using F = mk::at::FlashCfg<C, HD>;
+  auto* kernel = &mk::at::flash_kernel<T, C, HD, PAGED>;
+  static bool done[kMaxDevices] = {};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  constexpr bool BF = __is_same(T, mk::Bf16);
+  mk::at::FlashArgs fa;
+  fa.a = a;
+  fa.tq1 = 128 / a.group;
+  fa.least = 1;
+  fa.box_shift = 7;
+  if (!encode_map(&fa.q, a.q, BF, HD, a.group, a.rows, a.kv_heads, a.q_hs, a.q_ts,
+                  a.group * a.q_hs, a.group, fa.tq1))
+    return MK_ERR_UNSUPPORTED;
+  if (!F::E8) {
+    bool ok;
+    if (PAGED) {
+      if (a.c.page_shift < 7) fa.box_shift = a.c.page_shift;
+      const int kb = 1 << fa.box_shift, vb = kb < F::VK ? kb : F::VK;
+      ok = encode_map(&fa.k, a.c.k, BF, HD, a.c.page_size, a.c.kv_heads, a.c.n_pages,
+                      a.c.pos_stride, a.c.head_stride, a.c.page_stride, kb, 1) &&
+           encode_map(&fa.v, a.c.v, BF, HD, a.c.page_size, a.c.kv_heads, a.c.n_pages,
+                      a.c.pos_stride, a.c.head_stride, a.c.page_stride, vb, 1);
+    } else {
+      ok = encode_map(&fa.k, a.k, BF, HD, a.rows, a.kv_heads, 1, a.k_ts, a.k_hs, 0, mk::at::KEYS,
+                      1) &&
+           encode_map(&fa.v, a.v, BF, HD, a.rows, a.kv_heads, 1, a.v_ts, a.v_hs, 0, F::VK, 1);
+    }
+    if (!ok) return MK_ERR_UNSUPPORTED;
+  } else {
+    fa.k = fa.v = fa.q;
+  }
+  int ctas = sms;
+  constexpr int ROWS = F::NQ * 128;
+  while (mk::at::partial_bytes(ctas, ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
+  const mk::at::Partials p = mk::at::carve(ws, ctas, ROWS, HD);
+  kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
+  const int rc = launched();
+  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, ROWS, F::NQ * fa.tq1, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -406,9 +495,6 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   if (rc != MK_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
-  unsigned blocks;
-  rc = blocks_for((long long)rows * q_heads, 4, &blocks);
-  if (rc != MK_OK) return rc;
   by_half_type(dtype, [&](auto t) {
     by_head_dim(cache->head_dim, [&](auto d) {
       using T = typename decltype(t)::type;
@@ -420,13 +506,12 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
       else if (unit <= 16)
         rc = e8 ? launch_few<T, mk::E4m3, HD, 2>(a, workspace, dev, sms, st)
                 : launch_few<T, T, HD, 2>(a, workspace, dev, sms, st);
-      else if (e8)
-        mk::at::attn_simple_kernel<T, mk::E4m3, HD, true><<<blocks, 128, 0, st>>>(a);
       else
-        mk::at::attn_simple_kernel<T, T, HD, true><<<blocks, 128, 0, st>>>(a);
+        rc = e8 ? launch_flash<T, mk::E4m3, HD, true>(a, workspace, dev, sms, st)
+                : launch_flash<T, T, HD, true>(a, workspace, dev, sms, st);
     });
   });
-  return rc != MK_OK ? rc : launched();
+  return rc;
 }
 
 int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,
@@ -445,17 +530,17 @@ int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int
   a.k_hs = k_hs;
   a.v_ts = v_ts;
   a.v_hs = v_hs;
-  unsigned blocks;
-  rc = blocks_for((long long)rows * q_heads, 4, &blocks);
+  int dev, sms;
+  rc = device_sms(&dev, &sms);
   if (rc != MK_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_half_type(dtype, [&](auto t) {
     by_head_dim(head_dim, [&](auto d) {
       using T = typename decltype(t)::type;
-      mk::at::attn_simple_kernel<T, T, decltype(d)::value, false><<<blocks, 128, 0, st>>>(a);
+      rc = launch_flash<T, T, decltype(d)::value, false>(a, workspace, dev, sms, st);
     });
   });
-  return launched();
+  return rc;
 }
 
 }  // extern "C"

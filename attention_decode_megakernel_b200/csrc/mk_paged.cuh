@@ -18,9 +18,11 @@
 // the order of the head's dims inside a step is free as long as Q has the
 // same.  Score columns turn into weight rows by movmatrix.
 //
-// Softmax: m is raised only when a score passes it by 8 (weights up to 2^8
-// fit both 16-bit types, and their rounding is relative), so most subtiles
-// need one vote and no rescaling.  8-bit caches: codes go to fp16, exactly,
+// Softmax: weights are 2^(x - m), and m is raised only when a score passes it
+// by RAISE, so most subtiles need one vote and no rescaling.  bf16 weights
+// start at 1 and stay below 2^8, their rounding relative throughout; fp16
+// ones start at 2^7 and stay below 2^15 (LIFT), so that weights down to 2^-21
+// of the largest are normal numbers.  8-bit caches: codes go to fp16, exactly,
 // as do queries after a power of two for each row; the key row's scale
 // multiplies its scores and log2 of the value row's scale is added to them,
 // so that weights stay in fp16's range; their sum is taken without it.
@@ -35,6 +37,12 @@ namespace at {
 constexpr int FEW_WARPS = 4;
 constexpr int FEW_KEYS = 16 * FEW_WARPS;  // keys of a tile: 16 a warp
 constexpr int FEW_THREADS = 32 * FEW_WARPS;
+
+// The weight of the score that sets m is 2^LIFT, the largest one 2^RAISE.
+template <class M>
+struct Weights {
+  static constexpr float LIFT = __is_same(M, Fp16) ? 7.f : 0.f, RAISE = LIFT + 8.f;
+};
 
 template <class C, int HD, int NT>
 struct FewCfg {
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                             take);
         }
       }
-      ahead.next(line);
+      ahead.skip(line, 1);
     }
     cp_async_commit();
   };
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   while (at.left > 0) {
     // ---- one segment: the tiles of one unit that lie in this share
     const Cursor<FEW_KEYS> u = at;
-    const int seg = u.n - u.j < at.left ? u.n - u.j : at.left;
+    const int seg = u.segment();
     // queries: row r is token r / group of the tile, head r % group
     uint32_t q[NT][STEPS][2];
     float qs[NT][2];
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             if constexpr (E8) x = fmaf(x, kc[e >> 1], vl[e >> 1]);
             if (key + 16 > sure && key + g + 8 * (e >> 1) >= limit[nt][e & 1]) x = -INFINITY;
             s[nt][e] = x;
-            rise |= x > m[nt][e & 1] + 8.f;
+            rise |= x > m[nt][e & 1] + Weights<M>::RAISE;
           }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              top = fmaxf(top, m[nt][x]);
+              top = fmaxf(top - Weights<M>::LIFT, m[nt][x]);
               const float f = top == -INFINITY ? 1.f : ex2(m[nt][x] - top);
               m[nt][x] = top;
               l[nt][x] *= f;
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
       }
       stage = stage + 1 == STAGES ? 0 : stage + 1;
-      at.next(line);
+      at.skip(line, 1);
     }
 
     // ---- join the warps and write the segment

@@ -54,7 +54,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   s.n_new = hi - lo;
   s.len = s.n_new;
   if (a.table) {
-    const long long room = (long long)a.table_stride << a.c.page_shift;
+    long long room = (long long)a.table_stride << a.c.page_shift;
+    if (room > 1 << 30) room = 1 << 30;  // positions stay clear of 32 bits' end
     const int len = a.seq_lens[b];
     s.len = len < 0 ? 0 : len > room ? int(room) : len;
   }
@@ -102,9 +103,12 @@ struct Cursor {
   int b, h, i, j, n, nq;
   int left;  // tiles of this CTA's share from here on
 
-  __device__ void next(const Line<KT>& line) {
-    --left;
-    if (++j < n || left <= 0) return;
+  // tiles of the present unit that lie in this share
+  __device__ int segment() const { return n - j < left ? n - j : left; }
+  __device__ void skip(const Line<KT>& line, int tiles) {
+    left -= tiles;
+    j += tiles;
+    if (j < n || left <= 0) return;
     j = 0;
     if (++i == nq) {
       i = 0;

@@ -482,10 +482,11 @@ size_t mk_attn_ws_bytes(int head_dim);
  * the weights are rounded to 16 bits before they multiply the values.
  *   q, out [rows][q_heads][head_dim] device, dtype MK_BF16 or MK_FP16; query
  *     head h reads key head h / (q_heads / kv_heads); q_heads a multiple of
- *     the cache's kv_heads; the cache of the same dtype or MK_E4M3
+ *     the cache's kv_heads, 128 times at most (else MK_ERR_UNSUPPORTED); the
+ *     cache of the same dtype or MK_E4M3
  *   block_table device int32 [batch][table_stride]; seq_lens device int32
- *     [batch], held to 0 .. table_stride * page_size; a page number outside
- *     the cache stands for keys and values of zero
+ *     [batch], held to 0 .. table_stride * page_size (and to 2^30); a page
+ *     number outside the cache stands for keys and values of zero
  *   cu_q device int32 [batch + 1], from 0, not decreasing, at most `rows`;
  *     rows from cu_q[batch] on are left as they were
  *   lse device float32 [rows][q_heads] or NULL: the natural logarithm of the

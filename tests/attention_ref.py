@@ -10,8 +10,13 @@ operation's own roundings (u = 2^-24):
 * every weight p is rounded once to the values' type (eps / 2 relative; an
   e4m3 cache's values are multiplied as fp16), and so is the output;
 * numerator and denominator each carry d and 1000 u for sums and rescaling.
+* fp16 weights are 2^7 or more at the largest, and below 2^-14 they are rounded
+  to steps of 2^-24: each is off by up to 2^-25, in numbers whose sum is 2^7 or
+  more.  Weights that carry the scale s of an e4m3 row multiply codes v / s: the sum
+  of weights then is 2^7 / s or more at the row of the largest one.
 With A = sum p |v| / sum p the output is off by at most
-  eps_out / 2 |o| + A (eps_w / 2 + 2 (d + 2^-21 + 1000 u)),
+  eps_out / 2 |o| + A (eps_w / 2 + 2 (d + 2^-21 + 1000 u))
+  + (fp16 weights) 2^-32 sum |v / s| max s over the row's keys,
 and lse by d + 2^-21 + 1000 u + 4 u |lse|.
 """
 import math
@@ -84,9 +89,10 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def attend(q, k, v, seen, scale, out_type, weight_type):
+def attend(q, k, v, seen, scale, out_type, weight_type, v_scale=None):
     """One sequence: q [T][hq][hd], k, v [n][hk][hd] (64 bits), row t sees the
-    keys 0 .. seen[t] - 1.  Returns (out, lse, out's bound, lse's bound)."""
+    keys 0 .. seen[t] - 1; v_scale [n][hk] of an e4m3 cache.  Returns (out, lse,
+    out's bound, lse's bound)."""
     T, hq, hd = q.shape
     n, hk = k.shape[0], k.shape[1]
     g = hq // hk
@@ -110,6 +116,10 @@ def attend(q, k, v, seen, scale, out_type, weight_type):
         a = p @ vh.abs()
         out[:, h] = torch.where(some[:, None], o, 0.0)
         tol[:, h] = half_step(out_type) * o.abs() + a * (half_step(weight_type) + 2 * d[:, None])
+        if weight_type == torch.float16:
+            s = torch.ones(n, dtype=torch.float64) if v_scale is None else v_scale[:, h // g].double()
+            top = s[None].expand(T, n).masked_fill(hidden, 0).amax(-1)
+            tol[:, h] += 2.0 ** -32 * top[:, None] * ((~hidden).double() @ (vh.abs() / s[:, None]))
         # results below the type's normal range are rounded to its smallest step
         tol[:, h] += torch.finfo(out_type).smallest_normal * torch.finfo(out_type).eps
         lse[:, h] = le

@@ -47,6 +47,8 @@ def make_paged(gen, lens, heads, hd, size, kind, layout="hpd", spread=1.0, spare
                 x *= torch.exp(torch.randn(n, heads, 1, generator=gen, device="cuda") / 2)
                 codes, scale = ref.to_e4m3(x.cpu())
                 kv.append(codes * scale[..., None])
+                if i == 1:
+                    kv.append(scale)
                 stored = codes.float().to(E4).view(torch.uint8).cuda()
             else:
                 stored = x.to(kind)
@@ -85,7 +87,7 @@ def run_paged(mk, gen, new, lens, hq, hk, hd, size, dtype, kind, layout="hpd", p
         seen = [max(0, n - t + i + 1) for i in range(t)]
         want = ref.attend(q[first:first + t].cpu().double(), rows[b][0], rows[b][1], seen,
                           hd ** -0.5 if scale is None else scale, dtype,
-                          HF if kind == E4 else dtype)
+                          HF if kind == E4 else dtype, rows[b][2] if kind == E4 else None)
         ref.check(out[first:first + t], want[0], want[2], "out of sequence %d" % b)
         ref.check(lse[first:first + t], want[1], want[3], "lse of sequence %d" % b)
         first += t
@@ -161,7 +163,8 @@ def test_paged_rising_scores(mk, kind, t):
                   lse=lse)
     torch.cuda.synchronize()
     want = ref.attend(q.cpu().double(), kb.cpu().double(), vb.cpu().double(),
-                      [n - t + i + 1 for i in range(t)], hd ** -0.5, BF, HF if kind == E4 else BF)
+                      [n - t + i + 1 for i in range(t)], hd ** -0.5, BF, HF if kind == E4 else BF,
+                      pool[3][slots // 16, :, slots % 16].cpu() if kind == E4 else None)
     ref.check(out, want[0], want[2], "out")
     ref.check(lse, want[1], want[3], "lse")
 
@@ -176,7 +179,7 @@ def test_paged_pages_outside_the_cache(mk, kind, t):
     pool, table, rows = make_paged(gen, lens, 2, 64, 16, kind)
     table[0, 3], table[0, 7], table[1, 1] = -1, pool[0].shape[0], -(1 << 31)
     for b, p in ((0, 3), (0, 7), (1, 1)):
-        for x in rows[b]:
+        for x in rows[b][:2]:
             x[16 * p:16 * p + 16] = 0
     held = table.shape[1] * 16
     assert held == 208
@@ -184,6 +187,10 @@ def test_paged_pages_outside_the_cache(mk, kind, t):
     table[0, 12] = -5  # the positions 192 .. 207 are zeros too
     for x in (0, 1):
         rows[0][x] = torch.cat([rows[0][x][:192], torch.zeros(16, 2, 64, dtype=torch.float64)])
+    if kind == E4:  # rows of zeros count with a scale of one
+        for b, p in ((0, 3), (0, 7), (1, 1)):
+            rows[b][2][16 * p:16 * p + 16] = 1
+        rows[0][2] = torch.cat([rows[0][2][:192], torch.ones(16, 2, dtype=torch.float64)])
     q = torch.randn(2 * t, 4, 64, generator=gen, device="cuda").to(BF)
     out = torch.empty_like(q)
     cu = torch.tensor([0, t, 2 * t], dtype=torch.int32, device="cuda")
@@ -192,7 +199,8 @@ def test_paged_pages_outside_the_cache(mk, kind, t):
     torch.cuda.synchronize()
     for b, n in enumerate((held, 77)):
         want = ref.attend(q[b * t:(b + 1) * t].cpu().double(), rows[b][0], rows[b][1],
-                          [n - t + i + 1 for i in range(t)], 0.125, BF, HF if kind == E4 else BF)
+                          [n - t + i + 1 for i in range(t)], 0.125, BF, HF if kind == E4 else BF,
+                          rows[b][2] if kind == E4 else None)
         ref.check(out[b * t:(b + 1) * t], want[0], want[2], "out")
 
 
@@ -221,7 +229,8 @@ def test_paged_offsets_past_32_bits(mk, kind, t):
                   torch.tensor([0, t], dtype=torch.int32, device="cuda"), out)
     torch.cuda.synchronize()
     want = ref.attend(q.cpu().double(), kb.cpu().double(), vb.cpu().double(),
-                      [n - t + i + 1 for i in range(t)], hd ** -0.5, BF, HF if kind == E4 else BF)
+                      [n - t + i + 1 for i in range(t)], hd ** -0.5, BF, HF if kind == E4 else BF,
+                      s[1][slots // size, :, slots % size].cpu() if kind == E4 else None)
     ref.check(out, want[0], want[2], "out")
 
 
