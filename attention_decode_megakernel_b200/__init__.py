@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
+import struct
 from typing import Dict, Optional
 
 import numpy as np
@@ -57,7 +58,7 @@ class mk_weights(C.Structure):
 
 class mk_rope(C.Structure):
     _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float),
-                ("turns", C.c_double * 128)]
+                ("turns", C.c_uint64 * 128)]
 
 
 class mk_kv_cache(C.Structure):
@@ -378,59 +379,92 @@ def gemv_w4(codes, scales, x, y, stream=None):
 # Tensors are device tensors; rows are [token][head][dim] views with any token
 # and head distance (a slice of a fused projection, say).  Without `stream` a
 # call runs on torch's current stream of the tensors' device.
+#
+# A decoded token's calls take a few microseconds on the device, less than
+# ctypes needs for twenty arguments one by one.  So these five go through
+# libmk.so's mkw_ entries, which take the C ABI's arguments in its order as one
+# block of 64-bit words (floats as doubles) and call the entry of include/mk.h.
 
-_DTYPES = {}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+_torch = None
+_DTYPES = {}
 
 
-def _dtype(t, what):
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2,
-                        torch.float8_e4m3fn: 3})
-    code = _DTYPES.get(t.dtype)
+def _torch_types():
+    """Import torch for the calls below; code of each row type."""
+    global _torch
+    import torch
+    _torch = torch
+    _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2,
+                    torch.float8_e4m3fn: 3})
+    return _DTYPES
+
+
+def _code(dtype, what):
+    code = (_DTYPES or _torch_types()).get(dtype)
     if code is None:
-        raise ValueError("%s: %s is not a supported type" % (what, t.dtype))
+        raise ValueError("%s: %s is not a supported type" % (what, dtype))
     return code
 
 
-def _rows(t, what, shape=None, like=None):
+def _rows(t, what, shape, dtype, device):
     """(pointer, token distance, head distance) of a [token][head][dim] view."""
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError("%s must be [token][head][dim]%s, got %s"
-                         % (what, "" if shape is None else " = %s" % (shape,), tuple(t.shape)))
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError("%s must have the type and device of the other rows" % what)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError("%s must be [token][head][dim] = %s of %s on the device of the other "
+                         "rows, got %s of %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
     ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] > 1:
+    if ds != 1:
         raise ValueError("the dims of a head of %s must lie side by side" % what)
     # a distance that is never walked is whatever torch left there
-    return t.data_ptr(), ts if t.shape[0] > 1 else 0, hs if t.shape[1] > 1 else 0
+    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
 
-def _vector(t, what, dtype, shape, like):
-    import torch
-    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != shape or not t.is_contiguous() \
-            or t.device != like.device:
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (what, dtype, shape, like.device))
+def _vector(t, what, dtype, shape, device):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device \
+            or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, %s of %s on the device of the rows, got %s of %s"
+                         % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
     return t.data_ptr()
 
 
-def _launch(fn, what, device, stream, *args):
-    """Call fn(*args, stream) with the tensors' device current."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError("%s: the tensors must be on a CUDA device" % what)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc != MK_OK:
-        raise MkError(rc, what)
+def _head_rows(t, what):
+    """Shape [token][head][dim], type, its code and device index of the leading tensor."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [token][head][dim], got %s" % (what, tuple(t.shape)))
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("%s must be on a CUDA device" % what)
+    return t.shape, t.dtype, _code(t.dtype, what), device
+
+
+class _Call:
+    """One mkw_ entry: packs its arguments and runs it with `device` current."""
+
+    def __init__(self, name, words):
+        self.name, self.pack, self.fn = name, struct.Struct(words + "q").pack, None
+
+    def __call__(self, device, stream, *args):
+        if self.fn is None:
+            fn = getattr(lib(), self.name.replace("mk_", "mkw_"))
+            fn.restype, fn.argtypes = C.c_int, [C.c_char_p]
+            self.fn = fn
+        if stream is None:
+            stream = _torch._C._cuda_getCurrentRawStream(device)
+        block = self.pack(*args, stream)
+        if device == _torch._C._cuda_getDevice():
+            rc = self.fn(block)
+        else:
+            with _torch.cuda.device(device):
+                rc = self.fn(block)
+        if rc != MK_OK:
+            raise MkError(rc, self.name)
+
+
+_norm_rope_call = _Call("mk_qk_norm_rope", "20qdq")
+_kv_write_call = _Call("mk_kv_write", "10q")
+_kv_read_call = _Call("mk_kv_read", "10q")
+_paged_call = _Call("mk_attn_paged", "15qd3q")
+_packed_call = _Call("mk_attn_packed", "19qd3q")
 
 
 class Rope:
@@ -455,26 +489,24 @@ def qk_norm_rope(rope, q, k, positions, q_out=None, k_out=None, q_gain=None, k_g
     """RMSNorm (where a gain [head_dim] is given) and rotation of every head of
     q [tokens][q_heads][head_dim] and k [tokens][kv_heads][head_dim] (or None),
     by positions int32 [tokens]; in place where no output is given."""
-    q_out = q if q_out is None else q_out
-    tokens, heads, hd = q.shape
-    qp, qts, qhs = _rows(q, "q")
-    op, ots, ohs = _rows(q_out, "q_out", (tokens, heads, hd), q)
+    shape, dtype, code, dev = _head_rows(q, "q")
+    tokens, heads, hd = shape
+    qp, qts, qhs = _rows(q, "q", shape, dtype, dev)
+    op, ots, ohs = (qp, qts, qhs) if q_out is None else _rows(q_out, "q_out", shape, dtype, dev)
     kp = kts = khs = okp = okts = okhs = kv_heads = 0
     if k is not None:
-        kv_heads = k.shape[1]
-        k_out = k if k_out is None else k_out
-        kp, kts, khs = _rows(k, "k", (tokens, kv_heads, hd), q)
-        okp, okts, okhs = _rows(k_out, "k_out", (tokens, kv_heads, hd), q)
-    gains = []
-    for g, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if g is not None and (g.dtype != q.dtype or g.shape != (hd,) or g.stride(0) != 1
-                              or g.device != q.device):
-            raise ValueError("%s must be [head_dim] of the rows' type and device" % what)
-        gains.append(None if g is None else g.data_ptr())
-    pos = _vector(positions, "positions", "int32", (tokens,), q)
-    _launch(lib().mk_qk_norm_rope, "mk_qk_norm_rope", q.device, stream, rope.address, qp, qts, qhs,
-            kp, kts, khs, gains[0], gains[1], pos, op, ots, ohs, okp, okts, okhs, tokens, heads,
-            kv_heads, hd, eps, _dtype(q, "q"))
+        kshape = k.shape
+        kv_heads = kshape[1]
+        if kshape != (tokens, kv_heads, hd):
+            raise ValueError("k must be [tokens][kv_heads][head_dim] beside q")
+        kp, kts, khs = _rows(k, "k", kshape, dtype, dev)
+        okp, okts, okhs = (kp, kts, khs) if k_out is None else _rows(k_out, "k_out", kshape, dtype,
+                                                                     dev)
+    qg = 0 if q_gain is None else _vector(q_gain, "q_gain", dtype, (hd,), dev)
+    kg = 0 if k_gain is None else _vector(k_gain, "k_gain", dtype, (hd,), dev)
+    pos = _vector(positions, "positions", _torch.int32, (tokens,), dev)
+    _norm_rope_call(dev, stream, rope.address, qp, qts, qhs, kp, kts, khs, qg, kg, pos, op, ots,
+                    ohs, okp, okts, okhs, tokens, heads, kv_heads, hd, eps, code)
 
 
 class KvCache:
@@ -488,14 +520,15 @@ class KvCache:
             raise ValueError("k and v must be [page][kv_head][position][dim] views alike, "
                              "dims side by side")
         n, heads, size, hd = k.shape
-        code = _dtype(k, "cache")
+        code = _code(k.dtype, "cache")
+        self.device = k.get_device()
         for s in (k_scale, v_scale):
             if (code == 3) != (s is not None):
                 raise ValueError("scales belong to a float8_e4m3fn cache")
             if s is not None:
-                _vector(s, "scales", "float32", (n, heads, size), k)
+                _vector(s, "scales", _torch.float32, (n, heads, size), self.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.kv_heads, self.head_dim, self.page_size, self.device = heads, hd, size, k.device
+        self.kv_heads, self.head_dim, self.page_size = heads, hd, size
         ps, hs, ts = k.stride()[:3]
         self.c = mk_kv_cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                              ps if n > 1 else 0, hs if heads > 1 else 0, ts, n, size, heads, hd,
@@ -503,31 +536,31 @@ class KvCache:
         self.address = C.addressof(self.c)
 
 
+def _move_args(cache, k, v, slots):
+    shape, dtype, code, dev = _head_rows(k, "k")
+    tokens = shape[0]
+    if dev != cache.device or shape != (tokens, cache.kv_heads, cache.head_dim):
+        raise ValueError("rows of this cache must be [tokens][%d][%d] on its device"
+                         % (cache.kv_heads, cache.head_dim))
+    kp, kts, khs = _rows(k, "k", shape, dtype, dev)
+    vp, vts, vhs = _rows(v, "v", shape, dtype, dev)
+    sp = _vector(slots, "slots", _torch.int64, (tokens,), dev)
+    return dev, (kp, kts, khs, vp, vts, vhs), sp, tokens, code
+
+
 def kv_write(cache, k, v, slots, stream=None):
     """Rows k, v [tokens][kv_heads][head_dim] (bfloat16, float16 or float32) into
     the cache: token t to slot slots[t] = page * page_size + position (int64);
     a slot outside the cache (-1) skips its token."""
-    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
-    kp, kts, khs = _rows(k, "k", shape)
-    vp, vts, vhs = _rows(v, "v", shape, k)
-    sp = _vector(slots, "slots", "int64", shape[:1], cache)
-    if k.device != cache.device:
-        raise ValueError("the rows must be on the cache's device")
-    _launch(lib().mk_kv_write, "mk_kv_write", cache.device, stream, cache.address, kp, kts, khs,
-            vp, vts, vhs, sp, shape[0], _dtype(k, "k"))
+    dev, rows, sp, tokens, code = _move_args(cache, k, v, slots)
+    _kv_write_call(dev, stream, cache.address, *rows, sp, tokens, code)
 
 
 def kv_read(cache, slots, k_out, v_out, stream=None):
     """The rows of `slots` as values into k_out, v_out [tokens][kv_heads][head_dim];
     rows of slots outside the cache stay as they were."""
-    shape = (k_out.shape[0], cache.kv_heads, cache.head_dim)
-    kp, kts, khs = _rows(k_out, "k_out", shape)
-    vp, vts, vhs = _rows(v_out, "v_out", shape, k_out)
-    sp = _vector(slots, "slots", "int64", shape[:1], cache)
-    if k_out.device != cache.device:
-        raise ValueError("the rows must be on the cache's device")
-    _launch(lib().mk_kv_read, "mk_kv_read", cache.device, stream, cache.address, sp, shape[0], kp,
-            kts, khs, vp, vts, vhs, _dtype(k_out, "k_out"))
+    dev, rows, sp, tokens, code = _move_args(cache, k_out, v_out, slots)
+    _kv_read_call(dev, stream, cache.address, sp, tokens, *rows, code)
 
 
 def attn_workspace(head_dim, device="cuda"):
@@ -540,14 +573,16 @@ def attn_workspace(head_dim, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _attn_outputs(q, out, lse, workspace):
-    op, ots, ohs = _rows(out, "out", tuple(q.shape), q)
-    lp = None if lse is None else _vector(lse, "lse", "float32", tuple(q.shape[:2]), q)
+def _attn_outputs(shape, dtype, dev, out, lse, workspace):
+    op, ots, ohs = _rows(out, "out", shape, dtype, dev)
+    lp = 0 if lse is None else _vector(lse, "lse", _torch.float32, (shape[0], shape[1]), dev)
     if workspace is None:
-        workspace = attn_workspace(q.shape[2], q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+        workspace = attn_workspace(shape[2], "cuda:%d" % dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the rows' device")
-    return op, ots, ohs, lp, workspace
+    # (a workspace made here lives on as long as the call needs it: its memory is
+    # handed out again in the stream's order only)
+    return op, ots, ohs, lp, workspace.data_ptr(), workspace.nbytes
 
 
 def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None, workspace=None,
@@ -557,37 +592,38 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     which lie in the pages block_table[b] (int32).  out as q; lse float32
     [rows][q_heads] or None; scale head_dim ** -0.5 by default.  Rows behind
     cu_q[-1] stay as they were."""
-    rows, heads, hd = q.shape
-    qp, qts, qhs = _rows(q, "q")
-    batch = seq_lens.shape[0]
-    if hd != cache.head_dim or q.device != cache.device:
+    shape, dtype, code, dev = _head_rows(q, "q")
+    rows, heads, hd = shape
+    if hd != cache.head_dim or dev != cache.device:
         raise ValueError("q must have the cache's head_dim and device")
+    qp, qts, qhs = _rows(q, "q", shape, dtype, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][pages]")
-    pages = block_table.shape[1]
-    tp = _vector(block_table, "block_table", "int32", (batch, pages), q)
-    sp = _vector(seq_lens, "seq_lens", "int32", (batch,), q)
-    cp = _vector(cu_q, "cu_q", "int32", (batch + 1,), q)
-    op, ots, ohs, lp, workspace = _attn_outputs(q, out, lse, workspace)
-    _launch(lib().mk_attn_paged, "mk_attn_paged", q.device, stream, cache.address, qp, qts, qhs,
-            tp, pages, sp, cp, op, ots, ohs, lp, rows, batch, heads,
-            hd ** -0.5 if scale is None else scale, _dtype(q, "q"), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    batch, pages = block_table.shape
+    i32 = _torch.int32
+    tp = _vector(block_table, "block_table", i32, (batch, pages), dev)
+    sp = _vector(seq_lens, "seq_lens", i32, (batch,), dev)
+    cp = _vector(cu_q, "cu_q", i32, (batch + 1,), dev)
+    op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
+    _paged_call(dev, stream, cache.address, qp, qts, qhs, tp, pages, sp, cp, op, ots, ohs, lp,
+                rows, batch, heads, hd ** -0.5 if scale is None else scale, code, wp, wn)
 
 
 def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, stream=None):
     """Causal attention of whole prompts packed one after another: rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [rows][q_heads][head_dim] and of k, v
     [rows][kv_heads][head_dim] are sequence b."""
-    rows, heads, hd = q.shape
-    kv_heads = k.shape[1]
-    qp, qts, qhs = _rows(q, "q")
-    kp, kts, khs = _rows(k, "k", (rows, kv_heads, hd), q)
-    vp, vts, vhs = _rows(v, "v", (rows, kv_heads, hd), q)
+    shape, dtype, code, dev = _head_rows(q, "q")
+    rows, heads, hd = shape
+    kshape = k.shape
+    if len(kshape) != 3 or kshape != (rows, kshape[1], hd):
+        raise ValueError("k must be [rows][kv_heads][head_dim] beside q")
+    qp, qts, qhs = _rows(q, "q", shape, dtype, dev)
+    kp, kts, khs = _rows(k, "k", kshape, dtype, dev)
+    vp, vts, vhs = _rows(v, "v", kshape, dtype, dev)
     batch = cu_seqlens.shape[0] - 1
-    cp = _vector(cu_seqlens, "cu_seqlens", "int32", (batch + 1,), q)
-    op, ots, ohs, lp, workspace = _attn_outputs(q, out, lse, workspace)
-    _launch(lib().mk_attn_packed, "mk_attn_packed", q.device, stream, qp, qts, qhs, kp, kts, khs,
-            vp, vts, vhs, cp, op, ots, ohs, lp, rows, batch, heads, kv_heads, hd,
-            hd ** -0.5 if scale is None else scale, _dtype(q, "q"), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    cp = _vector(cu_seqlens, "cu_seqlens", _torch.int32, (batch + 1,), dev)
+    op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
+    _packed_call(dev, stream, qp, qts, qhs, kp, kts, khs, vp, vts, vhs, cp, op, ots, ohs, lp,
+                 rows, batch, heads, kshape[1], hd, hd ** -0.5 if scale is None else scale, code,
+                 wp, wn)

@@ -1,0 +1,276 @@
+// mk_attn_ops.cu -- host side of attention over a paged cache and over packed
+// prompts (include/mk.h): checks, tensor maps, choice of a kernel, launches.
+#include "mk_flash.cuh"
+#include "mk_ops.cuh"
+#include "mk_paged.cuh"
+
+namespace {
+
+// What both attention calls check and fill in.
+int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, void* out,
+              int64_t o_ts, int64_t o_hs, float* lse, int rows, int batch, int q_heads,
+              int kv_heads, int head_dim, float scale, int dtype, const void* workspace,
+              size_t ws_bytes, mk::at::AttnArgs* a) {
+  if (rows < 0 || batch < 0 || q_heads <= 0 || kv_heads <= 0 || !half_type(dtype))
+    return MK_ERR_ARG;
+  if (!head_dim_ok(head_dim)) return MK_ERR_UNSUPPORTED;
+  if (q_heads % kv_heads) return MK_ERR_ARG;
+  if (q_heads / kv_heads > 128) return MK_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return MK_ERR_ARG;
+  if (rows == 0 || batch == 0) return MK_OK;
+  if (!rows_ok(q, q_ts, q_hs, 2) || !rows_ok(out, o_ts, o_hs, 2) || !cu_q || !aligned(cu_q, 4) ||
+      (lse && !aligned(lse, 4)))
+    return MK_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mk_attn_ws_bytes(head_dim))
+    return MK_ERR_ARG;
+  a->q = static_cast<const unsigned char*>(q);
+  a->out = static_cast<unsigned char*>(out);
+  a->lse = lse;
+  a->q_ts = q_ts;
+  a->q_hs = q_hs;
+  a->o_ts = o_ts;
+  a->o_hs = o_hs;
+  a->cu_q = cu_q;
+  a->rows = rows;
+  a->batch = batch;
+  a->q_heads = q_heads;
+  a->kv_heads = kv_heads;
+  a->group = q_heads / kv_heads;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  return MK_OK;
+}
+
+constexpr int kMaxDevices = 64;
+
+// The current device and its number of multiprocessors.
+int device_sms(int* dev, int* sms) {
+  static int known[kMaxDevices] = {};
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  if (!known[*dev] && cudaDeviceGetAttribute(&known[*dev], cudaDevAttrMultiProcessorCount, *dev) !=
+                          cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  *sms = known[*dev];
+  return MK_OK;
+}
+
+// The join of partial results, launched so that its CTAs are in place when the
+// kernel before it ends.
+template <class T, int HD>
+int launch_join(const mk::at::AttnArgs& a, const mk::at::Partials& p, int ctas, int rows, int tq,
+                cudaStream_t st) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
+  c.blockDim = dim3(mk::at::JOIN_ROWS * 32);
+  c.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  if (cudaLaunchKernelEx(&c, mk::at::join_kernel<T, HD>, a, p, rows, tq) != cudaSuccess) {
+    return launched();
+  }
+  return launched();
+}
+
+template <class T, class C, int HD, int NT>
+int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+  using F = mk::at::FewCfg<C, HD, NT>;
+  auto* kernel = &mk::at::attn_few_kernel<T, C, HD, NT>;
+  static bool done[kMaxDevices] = {};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  int ctas = sms;
+  while (mk::at::partial_bytes(ctas, F::ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
+  const mk::at::Partials p = mk::at::carve(ws, ctas, F::ROWS, HD);
+  const int tq = F::ROWS / a.group;
+  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, 1);
+  const int rc = launched();
+  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, F::ROWS, tq, st);
+}
+
+// cuTensorMapEncodeTiled through the runtime (no link against the driver library).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_tiled() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// A 4D view of 16-bit values, strides in values for the dims 1 .. 3, boxes of
+// 64 values by b1 by b2, in the 128-byte swizzle; outside the view reads as zero.
+bool encode_map(CUtensorMap* m, const void* base, bool bf16, long long d0, long long d1,
+                long long d2, long long d3, long long s1, long long s2, long long s3, int b1,
+                int b2) {
+  const EncodeFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2), cuuint64_t(d3)};
+  // the stride of a dim of one is never walked; zero is not a valid one
+  const cuuint64_t strides[3] = {s1 > 0 ? cuuint64_t(s1) * 2 : 16, s2 > 0 ? cuuint64_t(s2) * 2 : 16,
+                                 s3 > 0 ? cuuint64_t(s3) * 2 : 16};
+  const cuuint32_t box[4] = {64u, cuuint32_t(b1), cuuint32_t(b2), 1u}, step[4] = {1u, 1u, 1u, 1u};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, class C, int HD, bool PAGED>
+int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+  using F = mk::at::FlashCfg<C, HD>;
+  auto* kernel = &mk::at::flash_kernel<T, C, HD, PAGED>;
+  static bool done[kMaxDevices] = {};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  constexpr bool BF = __is_same(T, mk::Bf16);
+  mk::at::FlashArgs fa;
+  fa.a = a;
+  fa.tq1 = 128 / a.group;
+  fa.least = 1;
+  fa.box_shift = 7;
+  if (!encode_map(&fa.q, a.q, BF, HD, a.group, a.rows, a.kv_heads, a.q_hs, a.q_ts,
+                  a.group * a.q_hs, a.group, fa.tq1))
+    return MK_ERR_UNSUPPORTED;
+  if (!F::E8) {
+    bool ok;
+    if (PAGED) {
+      if (a.c.page_shift < 7) fa.box_shift = a.c.page_shift;
+      const int kb = 1 << fa.box_shift, vb = kb < F::VK ? kb : F::VK;
+      ok = encode_map(&fa.k, a.c.k, BF, HD, a.c.page_size, a.c.kv_heads, a.c.n_pages,
+                      a.c.pos_stride, a.c.head_stride, a.c.page_stride, kb, 1) &&
+           encode_map(&fa.v, a.c.v, BF, HD, a.c.page_size, a.c.kv_heads, a.c.n_pages,
+                      a.c.pos_stride, a.c.head_stride, a.c.page_stride, vb, 1);
+    } else {
+      ok = encode_map(&fa.k, a.k, BF, HD, a.rows, a.kv_heads, 1, a.k_ts, a.k_hs, 0, mk::at::KEYS,
+                      1) &&
+           encode_map(&fa.v, a.v, BF, HD, a.rows, a.kv_heads, 1, a.v_ts, a.v_hs, 0, F::VK, 1);
+    }
+    if (!ok) return MK_ERR_UNSUPPORTED;
+  } else {
+    fa.k = fa.v = fa.q;
+  }
+  int ctas = sms;
+  constexpr int ROWS = F::NQ * 128;
+  while (mk::at::partial_bytes(ctas, ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
+  const mk::at::Partials p = mk::at::carve(ws, ctas, ROWS, HD);
+  kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
+  const int rc = launched();
+  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, ROWS, F::NQ * fa.tq1, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mk_attn_ws_bytes(int head_dim) {
+  if (!head_dim_ok(head_dim)) return 0;
+  return size_t(40) << 20;
+}
+
+int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
+                  const int32_t* block_table, int table_stride, const int32_t* seq_lens,
+                  const int32_t* cu_q, void* out, int64_t o_ts, int64_t o_hs, float* lse, int rows,
+                  int batch, int q_heads, float scale, int dtype, void* workspace, size_t ws_bytes,
+                  void* stream) {
+  mk::at::AttnArgs a = {};
+  int rc = cache_view(cache, &a.c);
+  if (rc != MK_OK) return rc;
+  rc = attn_args(q, q_ts, q_hs, cu_q, out, o_ts, o_hs, lse, rows, batch, q_heads, cache->kv_heads,
+                 cache->head_dim, scale, dtype, workspace, ws_bytes, &a);
+  if (rc != MK_OK) return rc;
+  if (cache->dtype != MK_E4M3 && cache->dtype != dtype) return MK_ERR_ARG;
+  if (rows == 0 || batch == 0) return MK_OK;
+  if (!block_table || !aligned(block_table, 4) || table_stride <= 0 || !seq_lens ||
+      !aligned(seq_lens, 4))
+    return MK_ERR_ARG;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.seq_lens = seq_lens;
+  int dev, sms;
+  rc = device_sms(&dev, &sms);
+  if (rc != MK_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
+  by_half_type(dtype, [&](auto t) {
+    by_head_dim(cache->head_dim, [&](auto d) {
+      using T = typename decltype(t)::type;
+      constexpr int HD = decltype(d)::value;
+      const bool e8 = cache->dtype == MK_E4M3;
+      if (unit <= 8)
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 1>(a, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 1>(a, workspace, dev, sms, st);
+      else if (unit <= 16)
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 2>(a, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 2>(a, workspace, dev, sms, st);
+      else
+        rc = e8 ? launch_flash<T, mk::E4m3, HD, true>(a, workspace, dev, sms, st)
+                : launch_flash<T, T, HD, true>(a, workspace, dev, sms, st);
+    });
+  });
+  return rc;
+}
+
+int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,
+                   int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                   const int32_t* cu_seqlens, void* out, int64_t o_ts, int64_t o_hs, float* lse,
+                   int rows, int batch, int q_heads, int kv_heads, int head_dim, float scale,
+                   int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  mk::at::AttnArgs a = {};
+  int rc = attn_args(q, q_ts, q_hs, cu_seqlens, out, o_ts, o_hs, lse, rows, batch, q_heads,
+                     kv_heads, head_dim, scale, dtype, workspace, ws_bytes, &a);
+  if (rc != MK_OK || rows == 0 || batch == 0) return rc;
+  if (!rows_ok(k, k_ts, k_hs, 2) || !rows_ok(v, v_ts, v_hs, 2)) return MK_ERR_ARG;
+  a.k = static_cast<const unsigned char*>(k);
+  a.v = static_cast<const unsigned char*>(v);
+  a.k_ts = k_ts;
+  a.k_hs = k_hs;
+  a.v_ts = v_ts;
+  a.v_hs = v_hs;
+  int dev, sms;
+  rc = device_sms(&dev, &sms);
+  if (rc != MK_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  by_half_type(dtype, [&](auto t) {
+    by_head_dim(head_dim, [&](auto d) {
+      using T = typename decltype(t)::type;
+      rc = launch_flash<T, T, decltype(d)::value, false>(a, workspace, dev, sms, st);
+    });
+  });
+  return rc;
+}
+
+}  // extern "C"
+
+extern "C" {
+int mkw_attn_paged(const void* w) { return call(mk_attn_paged, w); }
+int mkw_attn_packed(const void* w) { return call(mk_attn_packed, w); }
+}  // extern "C"

@@ -1,0 +1,145 @@
+// mk_ops.cuh -- what the host sides of the operators share: status of a
+// launch, checks of rows and caches, choice of a kernel by type and head
+// dim, and the Python binding's calling form.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <tuple>
+
+#include "mk.h"
+#include "mk_rows.cuh"
+
+namespace {
+
+inline int launched() {
+  const cudaError_t r = cudaGetLastError();
+  if (r == cudaSuccess) return MK_OK;
+  return r == cudaErrorInvalidConfiguration || r == cudaErrorLaunchOutOfResources ? MK_ERR_LAUNCH
+                                                                                 : MK_ERR_CUDA;
+}
+
+inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+inline bool half_type(int dtype) { return dtype == MK_BF16 || dtype == MK_FP16; }
+inline int value_size(int dtype) { return dtype == MK_FP32 ? 4 : dtype == MK_E4M3 ? 1 : 2; }
+
+// Rows whose 16-byte pieces the kernels read and write.
+inline bool rows_ok(const void* p, int64_t ts, int64_t hs, int size) {
+  return p && aligned(p, 16) && ts >= 0 && hs >= 0 && (ts * size) % 16 == 0 &&
+         (hs * size) % 16 == 0 && ts < (int64_t(1) << 38) && hs < (int64_t(1) << 38);
+}
+
+inline bool head_dim_ok(int hd) { return hd == 64 || hd == 128 || hd == 256; }
+
+// MK_OK and the kernels' view of a cache, or the error of a bad one.
+inline int cache_view(const mk_kv_cache* c, mk::PagedView* v) {
+  if (!c || c->n_pages <= 0 || c->kv_heads <= 0 || c->page_size <= 0) return MK_ERR_ARG;
+  if (c->dtype != MK_BF16 && c->dtype != MK_FP16 && c->dtype != MK_E4M3) return MK_ERR_ARG;
+  if (!head_dim_ok(c->head_dim)) return MK_ERR_UNSUPPORTED;
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  if ((1 << shift) != c->page_size || c->page_size < 16 || c->page_size > 256)
+    return MK_ERR_UNSUPPORTED;
+  const int size = value_size(c->dtype);
+  if (!rows_ok(c->k, c->page_stride, c->head_stride, size) ||
+      !rows_ok(c->v, c->page_stride, c->pos_stride, size))
+    return MK_ERR_ARG;
+  // rows must not overlap
+  if (c->pos_stride < c->head_dim || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
+      (c->n_pages > 1 && c->page_stride < c->head_dim))
+    return MK_ERR_ARG;
+  if (c->dtype == MK_E4M3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) ||
+                              !aligned(c->v_scale, 4)))
+    return MK_ERR_ARG;
+  v->k = static_cast<unsigned char*>(c->k);
+  v->v = static_cast<unsigned char*>(c->v);
+  v->k_scale = c->k_scale;
+  v->v_scale = c->v_scale;
+  v->page_stride = c->page_stride;
+  v->head_stride = c->head_stride;
+  v->pos_stride = c->pos_stride;
+  v->n_pages = c->n_pages;
+  v->page_size = c->page_size;
+  v->page_shift = shift;
+  v->kv_heads = c->kv_heads;
+  v->head_dim = c->head_dim;
+  return MK_OK;
+}
+
+template <class T>
+struct Tag {
+  using type = T;
+};
+template <int N>
+struct Num {
+  static constexpr int value = N;
+};
+
+// f(Tag of the row type); f(Num of the head dim)
+template <class F>
+void by_row_type(int dtype, F f) {
+  if (dtype == MK_BF16) f(Tag<mk::Bf16>{});
+  else if (dtype == MK_FP16) f(Tag<mk::Fp16>{});
+  else f(Tag<mk::Fp32>{});
+}
+template <class F>
+void by_half_type(int dtype, F f) {
+  if (dtype == MK_BF16) f(Tag<mk::Bf16>{});
+  else f(Tag<mk::Fp16>{});
+}
+template <class F>
+void by_cache_type(int dtype, F f) {
+  if (dtype == MK_BF16) f(Tag<mk::Bf16>{});
+  else if (dtype == MK_FP16) f(Tag<mk::Fp16>{});
+  else f(Tag<mk::E4m3>{});
+}
+template <class F>
+void by_head_dim(int hd, F f) {
+  if (hd == 64) f(Num<64>{});
+  else if (hd == 128) f(Num<128>{});
+  else f(Num<256>{});
+}
+
+inline int blocks_for(long long items, int per_block, unsigned* blocks) {
+  const long long n = (items + per_block - 1) / per_block;
+  if (n > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
+  *blocks = unsigned(n);
+  return MK_OK;
+}
+
+// ---- the Python binding's calling form -------------------------------------
+// The arguments of the entry of the same name, in its order, as 64-bit words
+// (floats as doubles): one conversion in place of twenty.
+struct Words {
+  const unsigned char* p;
+  int64_t word() {
+    int64_t w;
+    std::memcpy(&w, p, 8);
+    p += 8;
+    return w;
+  }
+  template <class T>
+  operator T*() {
+    return reinterpret_cast<T*>(word());
+  }
+  operator int64_t() { return word(); }
+  operator int() { return int(word()); }
+  operator size_t() { return size_t(word()); }
+  operator float() {
+    double d;
+    std::memcpy(&d, p, 8);
+    p += 8;
+    return float(d);
+  }
+};
+// Calls f with its parameters read one after another (braces keep the order).
+template <class... P>
+int call(int (*f)(P...), const void* block) {
+  Words w{static_cast<const unsigned char*>(block)};
+  const std::tuple<P...> a{static_cast<P>(w)...};
+  return std::apply(f, a);
+}
+}  // namespace

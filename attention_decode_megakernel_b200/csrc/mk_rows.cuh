@@ -11,6 +11,17 @@
 
 namespace mk {
 
+// {a, b} times {x, y}, two products in one instruction.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 c, d;\n\t"
+      "mov.b64 c, {%0, %1};\n\t"
+      "mov.b64 d, {%2, %3};\n\t"
+      "mul.rn.f32x2 c, c, d;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
 struct Bf16 {};
 struct Fp16 {};
 struct Fp32 {};
@@ -34,6 +45,13 @@ struct RowType<Bf16> {
     __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&p);
   }
+  // the larger magnitudes of two pairs (a NaN gives way to a number)
+  __device__ static uint32_t max_abs2(uint32_t m, uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    __nv_bfloat162 p = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m),
+                               *reinterpret_cast<__nv_bfloat162*>(&w));
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
   __device__ static uint4 pack(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
@@ -55,6 +73,11 @@ struct RowType<Fp16> {
   }
   __device__ static uint32_t pack2(float a, float b) {
     __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
+  __device__ static uint32_t max_abs2(uint32_t m, uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    __half2 p = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&w));
     return *reinterpret_cast<uint32_t*>(&p);
   }
   __device__ static uint4 pack(const float (&f)[8]) {

@@ -394,7 +394,7 @@ typedef struct {
   int32_t rot_dim;      /* rotated values at the front of a head            */
   int32_t interleaved;  /* pairs (2i, 2i + 1); else (i, i + rot_dim / 2)     */
   float magnitude;      /* length of the rotation                            */
-  double turns[128];    /* turns per position of pair i: f_i / 2 pi          */
+  uint64_t turns[128];  /* turns per position of pair i, f_i / 2 pi, in 2^-64 */
 } mk_rope;
 
 /* Fill *r (host).  rot_dim a multiple of 16, at most 256 (else
@@ -409,8 +409,8 @@ int mk_rope_init(mk_rope *r, int rot_dim, int interleaved, double theta,
  * rotation of its first rot_dim values by the token's position (launch post,
  * kernel bullet list: "fused QKV + RoPE"; head norms as an option):
  *   y = x rsqrt(mean(x^2) + eps) gain;  (y_a, y_b) of pair i turned by
- *   positions[token] * turns[i] turns
- * in fp32 with the angle reduced in double; rounded once, on the way out.
+ *   positions[token] * turns[i] 2^-64 turns
+ * in fp32, the angle in 64-bit fixed point; rounded once, on the way out.
  *   q, q_out [tokens][q_heads][head_dim], k, k_out [tokens][kv_heads][head_dim]
  *   device, of `dtype` (MK_BF16, MK_FP16 or MK_FP32); an output may be its
  *   input (the same pointer and distances), and must not overlap otherwise;
