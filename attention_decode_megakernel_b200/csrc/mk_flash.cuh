@@ -53,7 +53,7 @@ struct FlashCfg {
   static constexpr int SOFT_WARPS = 4 * NQ;
   static constexpr int THREADS = 128 + SOFT_WARPS * 32 + (E8 ? 128 : 0);
   static constexpr size_t SMEM = 1024 + size_t(NQ) * Q_TILE + size_t(STAGES) * STAGE +
-                                 size_t(SCALES) * 3 * KEYS * 4 + (E8 ? 2 * NQ * 128 * 4 : 0);
+                                 size_t(SCALES) * 3 * KEYS * 4 + (E8 ? 4 * NQ * 128 * 4 : 0);
   // registers of a thread: launched with, softmax, the others
   static constexpr int REGS_SOFT = THREADS == 512 ? 200 : THREADS == 384 ? (NQ == 2 ? 216 : 232) : 0;
   static constexpr int REGS_REST = THREADS == 512 ? 56 : THREADS == 384 ? (NQ == 2 ? 72 : 136) : 0;
@@ -61,6 +61,28 @@ struct FlashCfg {
                     (65536 / THREADS / 8 * 8) * THREADS,
                 "the shares exceed what the block is launched with");
 };
+// A place in the ring of stages.  Keys and values share the ring but not the
+// barriers that say a stage is full: an issuer that takes only keys (or only
+// values) may be laps away from the others, where the parity of a shared barrier
+// would mean nothing.  `phase` has a bit for each stage, [0] of its next load
+// of keys and [1] of values.
+template <int STAGES>
+struct Ring {
+  int stage = 0;
+  uint32_t lap = 0, phase[2] = {0, 0};
+  __device__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      lap ^= 1;
+    }
+  }
+  __device__ uint32_t flip(int v) {  // the parity of this load, and on to the next
+    const uint32_t p = phase[v] >> stage & 1;
+    phase[v] ^= 1u << stage;
+    return p;
+  }
+};
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   if constexpr (N > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -80,7 +102,7 @@ struct FlashArgs {
 
 struct FlashBars {
   uint64_t q_full, q_ready, q_empty;
-  uint64_t full[8], empty[8];
+  uint64_t full[2][8], empty[8];  // full: of keys, of values
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t sc_full[8];
   uint32_t tmem;
@@ -89,23 +111,34 @@ struct FlashBars {
   Cursor<KEYS> start;
 };
 
+// Called by whole warps; the answer is the same in every lane.
 __device__ __forceinline__ bool flash_wait(uint64_t* bar, uint32_t parity, FlashBars* f) {
+  bool ok = true;
   uint64_t start = 0;
   while (!mbar_try_wait(bar, parity)) {
     const uint64_t now = global_ns();
     if (start == 0) start = now;
     if (now - start > uint64_t(FLASH_WAIT_NS) || *(volatile int*)&f->gave_up) {
       *(volatile int*)&f->gave_up = 1;
-      return false;
+      ok = false;
+      break;
     }
   }
-  return true;
+  return __all_sync(0xffffffffu, ok);
 }
-// The same for a warp whose first lane works between the waits: the others
-// stay with it.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, FlashBars* f) {
-  __syncwarp();
-  return flash_wait(bar, parity, f);
+// The cursor in a form that the compiler knows to be the same in every lane, so
+// that what is computed from it stays in the warp's uniform registers.
+__device__ __forceinline__ void make_uniform(Cursor<KEYS>& c) {
+  c.s.first = uniform(c.s.first);
+  c.s.n_new = uniform(c.s.n_new);
+  c.s.len = uniform(c.s.len);
+  c.b = uniform(c.b);
+  c.h = uniform(c.h);
+  c.i = uniform(c.i);
+  c.j = uniform(c.j);
+  c.n = uniform(c.n);
+  c.nq = uniform(c.nq);
+  c.left = uniform(c.left);
 }
 
 // {x0, x1} * {y, y} + {c, c}
@@ -144,8 +177,10 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   unsigned char* base_ptr = smem_raw + (base - smem_addr(smem_raw));
   const uint32_t sq = base, ring = base + NQ * F::Q_TILE;
   float* scales = reinterpret_cast<float*>(base_ptr + NQ * F::Q_TILE + STAGES * F::STAGE);
-  float* q_size = scales + F::SCALES * 3 * KEYS;  // [2][NQ * 128]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // sizes of the queries' rows, [4][NQ * 128]: with one stream the scores of two more
+  // segments may come before the softmax of one reads them
+  float* q_size = scales + F::SCALES * 3 * KEYS;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Line<KEYS> line{a, NQ * fa.tq1};
   const int tq1 = fa.tq1, tile_rows = tq1 * a.group;
 
@@ -164,10 +199,11 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   } else if (warp == 2 && lane == 0) {
     mbar_init(&f.q_full, 1);
     mbar_init(&f.q_ready, 4);
-    mbar_init(&f.q_empty, 1);
+    mbar_init(&f.q_empty, NQ);
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&f.full[i], E8 ? 4 : 1);
-      mbar_init(&f.empty[i], 1);
+      mbar_init(&f.full[0][i], E8 ? 4 : 1);
+      mbar_init(&f.full[1][i], E8 ? 4 : 1);
+      mbar_init(&f.empty[i], NQ);
       mbar_init(&f.sc_full[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -188,8 +224,9 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   griddep_launch_dependents();
-  const uint32_t tmem = f.tmem;
+  const uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
   Cursor<KEYS> at = f.start;
+  make_uniform(at);
 
   // streams of a unit: the second row tile may have no tokens
   auto streams = [&](const Cursor<KEYS>& u) {
@@ -210,18 +247,20 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     fewer_registers<F::REGS_REST>();
   if (warp == 0) {
     // ---- TMA producer: queries, and keys and values unless they are converted
-    int it = 0, seg_no = 0, issued = 0;
-    while (at.left > 0 && !f.gave_up) {
+    Ring<STAGES> to;
+    int seg_no = 0;
+    while (at.left > 0) {
       const int seg = at.segment(), ns = streams(at);
-      bool ok = seg_no == 0 || warp_wait(&f.q_empty, (seg_no - 1) & 1, &f);
+      bool ok = seg_no == 0 || flash_wait(&f.q_empty, (seg_no - 1) & 1, &f);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
-      __syncwarp();
-      if (lane < ns * CHUNKS) {
-        const int s = lane / CHUNKS, c = lane % CHUNKS;
-        tma_load_4d(sq + s * F::Q_TILE + c * (128 * 128), &fa.q, c * 64, 0,
-                    at.s.first + at.i * NQ * tq1 + s * tq1, at.h, &f.q_full);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
+        for (int s = 0; s < ns; ++s)
+          for (int c = 0; c < CHUNKS; ++c)
+            tma_load_4d(sq + s * F::Q_TILE + c * (128 * 128), &fa.q, c * 64, 0,
+                        at.s.first + at.i * NQ * tq1 + s * tq1, at.h, &f.q_full);
       }
+      __syncwarp();
       if constexpr (!E8) {
         const int limit = line.limit(at.s, at.i), end = at.j + seg;
         const int shift = PAGED ? fa.box_shift : 7;
@@ -238,28 +277,27 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           return page;
         };
         auto load = [&](bool v, int j, int pages) {
-          for (int p = 0; p < PARTS; ++p, ++it) {
-            const int st = it % STAGES;
-            if (it >= STAGES && !warp_wait(&f.empty[st], (it / STAGES - 1) & 1, &f)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&f.full[st], F::STAGE);
-            __syncwarp();
-            issued = it + 1;
+          for (int p = 0; p < PARTS; ++p, to.next()) {
+            const int st = to.stage;
+            // (a fresh barrier's phase before the first counts as complete)
+            if (!flash_wait(&f.empty[st], to.lap ^ 1, &f)) return false;
+            to.flip(v);
+            uint64_t* full = &f.full[v][st];
             const int rows = v && F::VK < (1 << shift) ? F::VK : 1 << shift;  // of a box
-            const int per_col = (v ? F::VK : KEYS) / rows, cols = v ? CHUNKS : F::KC;
-            for (int x0 = 0; x0 < per_col * cols; x0 += 32) {
-              const int x = x0 + lane, c = x / per_col, b = x % per_col;
-              const int row = b * rows;                     // in the stage
-              const int key = row + (v ? p * F::VK : 0);    // in the tile
-              const int page = __shfl_sync(0xffffffffu, pages, (key >> shift) & 31);
-              if (x < per_col * cols) {
-                const uint32_t dst =
-                    ring + st * F::STAGE + (c * (v ? F::VK : KEYS) + row) * 128;
-                const int dim = (c + (v ? 0 : p * F::KC)) * 64;
-                const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
-                                      : at.s.first + j * KEYS + key;
-                tma_load_4d(dst, v ? &fa.v : &fa.k, dim, pos, at.h, PAGED ? page : 0,
-                            &f.full[st]);
+            const int n_rows = v ? F::VK : KEYS, cols = v ? CHUNKS : F::KC;
+            if (elect_one()) mbar_arrive_expect_tx(full, F::STAGE);
+            for (int row = 0; row < n_rows; row += rows) {
+              const int key = row + (v ? p * F::VK : 0);  // in the tile
+              const int page = __shfl_sync(0xffffffffu, pages, key >> shift);
+              const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
+                                    : at.s.first + j * KEYS + key;
+              if (elect_one()) {
+                const uint32_t dst = ring + st * F::STAGE + row * 128;
+                for (int c = 0; c < cols; ++c)
+                  tma_load_4d(dst + c * (n_rows * 128), v ? &fa.v : &fa.k,
+                              (c + (v ? 0 : p * F::KC)) * 64, pos, at.h, PAGED ? page : 0, full);
               }
+              __syncwarp();
             }
           }
           return true;
@@ -280,165 +318,182 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         if (!ok) break;
       }
       at.skip(line, seg);
+      make_uniform(at);
       ++seg_no;
     }
     // copies in flight must land before the CTA can end
     if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f);
     if (!E8)
-      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) {
-        const uint64_t start = global_ns();
-        while (!mbar_try_wait(&f.full[i % STAGES], (i / STAGES) & 1))
-          if (global_ns() - start > uint64_t(FLASH_WAIT_NS)) break;
-      }
-  } else if (warp == 1) {
-    // ---- MMA issuer
+      for (int i = 0; i < STAGES; ++i)
+        for (int v = 0; v < 2; ++v) {  // the last load of each kind (of none: complete at once)
+          const uint64_t start = global_ns();
+          while (!mbar_try_wait(&f.full[v][i], (to.phase[v] >> i & 1) ^ 1))
+            if (global_ns() - start > uint64_t(FLASH_WAIT_NS)) break;
+        }
+  } else if (warp <= 2) {
+    // ---- MMA issuers.  Two streams: warp 1 + s issues the scores and outputs of
+    // stream s.  One stream: warp 1 issues the scores, warp 2 the outputs.
     constexpr uint32_t id_s = idesc_f16(BF, 128, KEYS, false), id_o = idesc_f16(BF, 128, HD, true);
-    int it = 0, seg_no = 0;
-    int cnt[2] = {0, 0};   // key tiles of a stream so far
-    int segs[2] = {0, 0};  // its segments so far: each ends with an epilogue that reads O
-    bool ok = true;
-    auto issue_s = [&](int slot, int q, int at_it) {
+    const int me = warp - 1;
+    Ring<STAGES> ring_at;
+    int seg_no = 0, cnt = 0, segs = 0;  // segments, own key tiles, own segments so far
+    auto on = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
+    auto issue_s = [&](int slot, int q, int st) {
       uint64_t qd = desc_k_major(sq + q * F::Q_TILE);
-#pragma unroll 1
-      for (int c = 0; c < CHUNKS; ++c, qd += 128 * 128 / 16) {
-        const int st = (at_it + c / F::KC) % STAGES;
-        const uint64_t kd = desc_k_major(ring + st * F::STAGE + (c % F::KC) * (KEYS * 128));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, c + k > 0);
+      for (int p = 0; p < PARTS; ++p, st = on(st)) {
+        uint64_t kd = desc_k_major(ring + st * F::STAGE);
+#pragma unroll
+        for (int c = 0; c < F::KC; ++c, qd += 128 * 128 / 16, kd += KEYS * 128 / 16)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, p + c + k > 0);
       }
     };
-    auto issue_o = [&](int slot, int s, int at_it, bool more) {
-#pragma unroll 1
-      for (int p = 0; p < PARTS; ++p) {
-        const int st = (at_it + p) % STAGES;
+    auto issue_o = [&](int slot, int s, int st, bool more) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p, st = on(st)) {
         const uint64_t vd = desc_mn_major(ring + st * F::STAGE, F::VK * 128);
-#pragma unroll 4
+#pragma unroll
         for (int k = 0; k < F::VK / 16; ++k)
           tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + (p * F::VK + k * 16) / 2,
                     vd + k * (2048 / 16), id_o, more || p + k > 0);
       }
     };
-    auto wait_parts = [&](int at_it) {
-      for (int p = 0; p < PARTS; ++p)
-        if (!warp_wait(&f.full[(at_it + p) % STAGES], ((at_it + p) / STAGES) & 1, &f))
-          return false;
-      return true;
-    };
-    auto release = [&](int at_it) {
-      for (int p = 0; p < PARTS; ++p) tc_commit(&f.empty[(at_it + p) % STAGES]);
-    };
-    // zero what lies behind the sequence in the V tile of stages at_it ..
-    auto clear_tail = [&](int at_it, int j, int len) {
-      if constexpr (!E8) {
-        if (len >= (j + 1) * KEYS) return;
-        for (int p = 0; p < PARTS; ++p) {
-          const int keep = len - j * KEYS - p * F::VK;
-          for (int x = lane; x < F::VK * 8; x += 32) {
-            if (x / 8 < keep) continue;
-            const uint32_t to = ring + ((at_it + p) % STAGES) * F::STAGE + x * 16;
+    // Waits for the operand in the ring's next stages and moves past it; its first stage.
+    auto take = [&](int v, int& first) {
+      first = ring_at.stage;
+      bool ok = true;
 #pragma unroll
+      for (int p = 0; p < PARTS; ++p, ring_at.next())
+        ok = ok && flash_wait(&f.full[v][ring_at.stage], ring_at.flip(v), &f);
+      return ok;
+    };
+    auto pass = [&] {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) ring_at.next();
+    };
+    auto release = [&](int st) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p, st = on(st)) tc_commit(&f.empty[st]);
+    };
+    // Zero what lies behind the sequence in a V tile (both streams' issuers do: zeros
+    // over zeros).
+    auto clear_tail = [&](int st, int j) {
+      if constexpr (!E8) {
+        const int keep = at.s.len - j * KEYS;
+        if (keep >= KEYS) return;
+        for (int p = 0; p < PARTS; ++p, st = on(st))
+          for (int x = lane; x < F::VK * 8; x += 32) {
+            if (x / 8 + p * F::VK < keep) continue;
+            const uint32_t to = ring + st * F::STAGE + x * 16;
             for (int c = 0; c < CHUNKS; ++c)
               asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + c * F::VK * 128),
                            "r"(0)
                            : "memory");
           }
-        }
         fence_async_smem();
         __syncwarp();
       }
     };
+    bool ok = true;
     while (at.left > 0 && ok) {
       const int seg = at.segment(), end = at.j + seg, ns = streams(at);
-      ok = warp_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f);
-      if (!ok) break;
-      int e[2] = {stream_end(at, 0, end), ns == 2 ? end : at.j};
-      bool first[2] = {true, true};
-      // O is free once the epilogue of the stream's last segment has read it
-      auto wait_o = [&](int s) {
-        return segs[s] == 0 || warp_wait(&f.o_empty[s], (segs[s] - 1) & 1, &f);
-      };
-      int k_it = it, v_it;
-      it += PARTS;
-      ok = wait_parts(k_it);
-      if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int s = 0; s < NQ; ++s)
-          if (at.j < e[s]) {
-            const int slot = NQ == 1 ? cnt[0] & 1 : s;
-            issue_s(slot, s, k_it);
-            tc_commit(&f.s_full[slot]);
-          }
-        release(k_it);
-        if (seg == 1) tc_commit(&f.q_empty);
-      }
-      for (int j = at.j; j < end && ok; ++j) {
-        const bool more = j + 1 < end;
-        bool have_k = false;
-        if (NQ == 1 && more) {
-          // the next tile's scores before this tile's output
-          k_it = it;
-          it += PARTS;
-          ok = wait_parts(k_it);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const int slot = (cnt[0] + 1) & 1;
-            issue_s(slot, 0, k_it);
-            tc_commit(&f.s_full[slot]);
-            release(k_it);
-            if (j + 2 == end) tc_commit(&f.q_empty);
-          }
-        }
-        v_it = it;
-        it += PARTS;
-        if (NQ == 2 && more) {
-          k_it = it;
-          it += PARTS;
-        }
-        ok = wait_parts(v_it);
+      // (whoever issues scores; the outputs' issuer of one stream may be two segments
+      // behind, where the barrier's parity says nothing)
+      if (NQ == 2 || me == 0)
+        ok = flash_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f);
+      int k_at, v_at;
+      if constexpr (NQ == 2) {
+        const bool active = me < ns;
+        const int e = !active ? at.j : me == 0 ? stream_end(at, 0, end) : end;
+        ok = ok && take(0, k_at);
         if (!ok) break;
-        clear_tail(v_it, j, at.s.len);
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) {
-          if (j >= e[s]) continue;
-          const int slot = NQ == 1 ? cnt[0] & 1 : s;
-          if (first[s]) ok = wait_o(s);
-          ok = ok && warp_wait(&f.p_full[slot], (NQ == 1 ? cnt[0] >> 1 : cnt[s]) & 1, &f);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            issue_o(slot, s, v_it, !first[s]);
-            tc_commit(&f.o_full[slot]);
+        tc_fence_after();
+        if (elect_one()) {
+          if (at.j < e) {
+            issue_s(me, me, k_at);
+            tc_commit(&f.s_full[me]);
           }
-          first[s] = false;
-          ++cnt[s];
-          if (NQ == 2 && j + 1 < e[s]) {
-            if (!have_k) {
-              ok = wait_parts(k_it);
-              if (!ok) break;
-              tc_fence_after();
-              have_k = true;
+          release(k_at);
+          if (seg == 1) tc_commit(&f.q_empty);
+        }
+        for (int j = at.j; j < end && ok; ++j) {
+          const bool more = j + 1 < end;
+          ok = take(1, v_at);
+          if (!ok) break;
+          if (j < e) {
+            clear_tail(v_at, j);
+            // O is free once the epilogue of the stream's last segment has read it
+            if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f);
+            ok = ok && flash_wait(&f.p_full[me], cnt & 1, &f);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_o(me, me, v_at, j > at.j);
+              tc_commit(&f.o_full[me]);
+              release(v_at);
             }
-            if (lane == 0) {
-              issue_s(s, s, k_it);
-              tc_commit(&f.s_full[s]);
+            ++cnt;
+          } else if (elect_one()) {
+            release(v_at);
+          }
+          if (more) {
+            ok = take(0, k_at);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if (j + 1 < e) {
+                issue_s(me, me, k_at);
+                tc_commit(&f.s_full[me]);
+              }
+              release(k_at);
+              if (j + 2 == end) tc_commit(&f.q_empty);
             }
           }
         }
-        if (!ok) break;
-        if (lane == 0) {
-          release(v_it);
-          if (NQ == 2 && more) release(k_it);
-          if (NQ == 2 && j + 2 == end) tc_commit(&f.q_empty);
+        if (active) {
+          // a stream without tiles here keeps step with its epilogues all the same
+          if (ok && e <= at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f);
+          ++segs;
         }
-      }
-      for (int s = 0; s < ns && ok; ++s) {
-        if (first[s]) ok = wait_o(s);  // a stream without tiles here: keep step with its epilogues
-        ++segs[s];
+      } else if (me == 0) {
+        for (int x = 0; x < seg && ok; ++x, ++cnt) {
+          ok = take(0, k_at);
+          // the scores' columns are free once the output has used the weights in them
+          if (ok && cnt > 1) ok = flash_wait(&f.o_full[cnt & 1], ((cnt >> 1) - 1) & 1, &f);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_s(cnt & 1, 0, k_at);
+            tc_commit(&f.s_full[cnt & 1]);
+            release(k_at);
+            if (x + 1 == seg) tc_commit(&f.q_empty);
+          }
+          if (x > 0) pass();         // the V tile behind it
+          if (x + 1 == seg) pass();  // the last one
+        }
+      } else {
+        pass();  // the first K tile
+        for (int j = at.j; j < end && ok; ++j, ++cnt) {
+          if (j + 1 < end) pass();
+          ok = take(1, v_at);
+          if (!ok) break;
+          clear_tail(v_at, j);
+          if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[0], (segs - 1) & 1, &f);
+          ok = ok && flash_wait(&f.p_full[cnt & 1], (cnt >> 1) & 1, &f);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_o(cnt & 1, 0, v_at, j > at.j);
+            tc_commit(&f.o_full[cnt & 1]);
+            release(v_at);
+          }
+        }
+        ++segs;
       }
       at.skip(line, seg);
+      make_uniform(at);
       ++seg_no;
     }
     __syncwarp();
@@ -459,7 +514,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
       const Cursor<KEYS> u = at;
       const int seg = u.segment(), end = u.j + seg;
       at.skip(line, seg);
-      const int parity_seg = seg_no++, tile0 = tiles - u.j;
+      make_uniform(at);
+      const int seg_at = seg_no++, tile0 = tiles - u.j;
       tiles += seg;
       if (s >= streams(u)) continue;
       const int e = stream_end(u, s, end);
@@ -479,7 +535,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         if constexpr (E8) ok = ok && flash_wait(&f.sc_full[(tile0 + j) & 7], (tile0 + j) >> 3 & 1, &f);
         // (the converters wrote it before the first tile's scales)
         if (RESCALE_Q && j == u.j)
-          c = a.scale_log2 * q_size[(parity_seg & 1) * NQ * 128 + s * 128 + r];
+          c = a.scale_log2 * q_size[(seg_at & 3) * NQ * 128 + s * 128 + r];
         if (!ok) break;
         tc_fence_after();
         if (any_live) {
@@ -626,7 +682,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     const int ct = tid - 128 - F::SOFT_WARPS * 32;
     constexpr int N = F::STAGE / 32 / 128;  // 16-code pieces of a thread and stage
     int it = 0, seg_no = 0, tiles = 0;
-    while (at.left > 0 && !*(volatile int*)&f.gave_up) {
+    while (at.left > 0) {
       const int seg = at.segment(), end = at.j + seg, ns = streams(at);
       bool ok = true;
       if constexpr (RESCALE_Q) {
@@ -646,7 +702,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           uint32_t ex = __float_as_uint(size) >> 23;
           ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
           const float down = __uint_as_float((254 - ex) << 23);
-          q_size[(seg_no & 1) * NQ * 128 + s * 128 + ct] = __uint_as_float(ex << 23);
+          q_size[(seg_no & 3) * NQ * 128 + s * 128 + ct] = __uint_as_float(ex << 23);
 #pragma unroll 4
           for (int x = 0; x < CHUNKS * 8; ++x) {
             const uint32_t p = row + (x >> 3) * (128 * 128) + (((x + ct) & 7) << 4);
@@ -759,20 +815,21 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&f.full[st]);
+        if (lane == 0) mbar_arrive(&f.full[v][st]);
 #pragma unroll
         for (int i = 0; i < N; ++i) cur[i] = next[i];
       }
       if (!ok) break;
       tiles += seg;
       at.skip(line, seg);
+      make_uniform(at);
       ++seg_no;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(f.tmem, 512);
 }
 
 }  // namespace at
