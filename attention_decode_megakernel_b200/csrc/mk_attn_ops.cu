@@ -60,21 +60,19 @@ int device_sms(int* dev, int* sms) {
 
 // The join of partial results, launched so that its CTAs are in place when the
 // kernel before it ends.
-template <class T, int HD>
-int launch_join(const mk::at::AttnArgs& a, const mk::at::Partials& p, int ctas, int rows, int tq,
+int launch_join(void (*kernel)(mk::at::AttnArgs, mk::at::Partials, int, int), dim3 grid,
+                const mk::at::AttnArgs& a, const mk::at::Partials& p, int rows, int tq,
                 cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
-  c.blockDim = dim3(mk::at::JOIN_ROWS * 32);
+  c.gridDim = grid;
+  c.blockDim = dim3(128);
   c.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
-  if (cudaLaunchKernelEx(&c, mk::at::join_kernel<T, HD>, a, p, rows, tq) != cudaSuccess) {
-    return launched();
-  }
+  cudaLaunchKernelEx(&c, kernel, a, p, rows, tq);
   return launched();
 }
 
@@ -97,7 +95,8 @@ int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream
   const int tq = F::ROWS / a.group;
   kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, 1);
   const int rc = launched();
-  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, F::ROWS, tq, st);
+  const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
+  return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);
 }
 
 // cuTensorMapEncodeTiled through the runtime (no link against the driver library).
@@ -184,7 +183,9 @@ int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStre
   const mk::at::Partials p = mk::at::carve(ws, ctas, ROWS, HD);
   kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
   const int rc = launched();
-  return rc != MK_OK ? rc : launch_join<T, HD>(a, p, ctas, ROWS, F::NQ * fa.tq1, st);
+  const int tq = F::NQ * fa.tq1;
+  const dim3 join(ctas, (tq * a.group + 31) / 32 * (HD / 64));
+  return rc != MK_OK ? rc : launch_join(mk::at::join_tiles_kernel<T, HD>, join, a, p, ROWS, tq, st);
 }
 
 }  // namespace

@@ -141,6 +141,18 @@ __device__ __forceinline__ void make_uniform(Cursor<KEYS>& c) {
   c.left = uniform(c.left);
 }
 
+// 32 bytes of a row: one access where the address allows it (rows start on 16).
+__device__ __forceinline__ void store32(unsigned char* p, const uint32_t* w) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // {x0, x1} * {y, y} + {c, c}
 __device__ __forceinline__ void fma2(float& x0, float& x1, float y, float c) {
   asm("{\n\t.reg .b64 a, b, d;\n\t"
@@ -631,41 +643,57 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
       const bool whole = u.j == 0 && seg == u.n;
       float l = l0 + l1;
       if (!ok) l = m = __int_as_float(0x7FC00000);  // a wait ran out: NaN
-      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int head = u.h * a.group + r % a.group;
       const long long row = u.s.first + (live ? token : 0);
-      const size_t slot_row =
-          (2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0)) * (NQ * 128) + s * tile_rows + r;
+      const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
+      const int part_row = s * tile_rows + r;
       if (any_live) {
+        // A thread has its row, 32 columns at a time.  A finished row leaves in whole
+        // 32-byte sectors; partial rows lie side by side, [column / 4][row] float4, so that
+        // a warp's store is 512 bytes in a piece.  (Trading values between lanes until rows
+        // leave in 64-byte pieces took 4900 cycles a segment at head_dim 128, all of it
+        // instructions; 16 bytes a lane straight to rows of fp32 10000.)
+        const bool none = e <= u.j;  // no tiles here: O is not this segment's
+        unsigned char* out = a.out + (row * a.o_ts + head * a.o_hs) * 2;
+        float4* pieces = reinterpret_cast<float4*>(part.o) +
+                         slot * (HD / 4) * (NQ * 128) + part_row;
+        float o[32];
+        tmem_ld32(lanes + 256 + s * HD, o);
 #pragma unroll 1
         for (int d = 0; d < HD; d += 32) {
-          float o[32];
-          tmem_ld32(lanes + 256 + s * HD + d, o);
+          float v[32];
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             pin(o[i]);
-            o[i] = e > u.j ? o[i] * inv : 0.f;
-            if (!ok) o[i] = l;
+            v[i] = o[i];
           }
-          if (live && whole) {
-            uint4* to = reinterpret_cast<uint4*>(a.out + (row * a.o_ts + head * a.o_hs + d) * 2);
+          if (d + 32 < HD) tmem_ld32(lanes + 256 + s * HD + d + 32, o);
+          if (none || !ok) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              to[i / 8] = make_uint4(
-                  RowType<T>::pack2(o[i], o[i + 1]), RowType<T>::pack2(o[i + 2], o[i + 3]),
-                  RowType<T>::pack2(o[i + 4], o[i + 5]), RowType<T>::pack2(o[i + 6], o[i + 7]));
-          } else if (live) {
-            float4* to = reinterpret_cast<float4*>(part.o + slot_row * HD + d);
+            for (int i = 0; i < 32; ++i) v[i] = ok ? 0.f : l;
+          }
+          if (!live) continue;
+          if (whole) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              mul2(v[i], v[i + 1], inv, inv);
+              w[i / 2] = RowType<T>::pack2(v[i], v[i + 1]);
+            }
+            store32(out + d * 2, w);
+            store32(out + d * 2 + 32, w + 8);
+          } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              to[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              pieces[(d + i) / 4 * (NQ * 128)] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
         if (live && whole) {
           if (a.lse) a.lse[row * a.q_heads + head] = row_lse(m, l);
         } else if (live) {
-          part.ml[slot_row] = make_float2(m, l);
+          part.ml[slot * (NQ * 128) + part_row] = make_float2(m, l);
         }
       }
       if (s == 0 && r == 0 && u.j == 0 && !whole) {

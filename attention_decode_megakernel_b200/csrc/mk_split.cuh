@@ -186,8 +186,9 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
   return c;
 }
 
-// Partial results in the workspace: for slot s the rows' weighted sums
-// [R][HD], their {maximum, sum} [R], and for each CTA the unit that it left unfinished.
+// Partial results in the workspace: for slot s the rows' weighted sums, [R][HD]
+// (few rows) or [HD / 4][R] float4 (tiles of rows), their {maximum, sum} [R], and
+// for each CTA the unit that it left unfinished.
 struct Left {
   int b, h, i;
   int more;  // CTAs behind this one that hold the rest; 0: nothing was left
@@ -276,6 +277,57 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
     }
   }
   if (a.lse && lane == 0) a.lse[(long long)(first + token) * a.q_heads + head] = row_lse(m, l);
+}
+
+// The same for partials [HD / 4][rows]: block (c, y) takes 32 rows, a lane for each,
+// and 64 columns, 16 to a warp.
+template <class T, int HD>
+__global__ void __launch_bounds__(128)
+    join_tiles_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows, int tq) {
+  griddep_wait();
+  const Left u = p.left[blockIdx.x];
+  if (u.more <= 0) return;
+  const Seq s = seq_of(a, u.b);
+  const int lane = threadIdx.x & 31, r = blockIdx.y / (HD / 64) * 32 + lane;
+  const int d = blockIdx.y % (HD / 64) * 64 + (threadIdx.x >> 5) * 16;
+  const int token = u.i * tq + r / a.group;
+  if (r >= tq * a.group || token >= s.n_new) return;
+  auto slot_of = [&](int k) {
+    return k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
+  };
+  float m = -INFINITY;
+  for (int k = 0; k <= u.more; ++k) m = fmaxf(m, p.ml[slot_of(k) * rows + r].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k <= u.more; ++k) {
+    const size_t slot = slot_of(k);
+    const float2 ml = p.ml[slot * rows + r];
+    const float f = exp2f(ml.x - base);
+    l += f * ml.y;
+    const float4* src = reinterpret_cast<const float4*>(p.o) + (slot * (HD / 4) + d / 4) * rows + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = src[i * rows];
+      o[4 * i] += f * x.x;
+      o[4 * i + 1] += f * x.y;
+      o[4 * i + 2] += f * x.z;
+      o[4 * i + 3] += f * x.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int head = u.h * a.group + r % a.group;
+  const long long row = s.first + token;
+  uint4* out = reinterpret_cast<uint4*>(a.out + (row * a.o_ts + head * a.o_hs + d) * 2);
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    out[i / 8] = make_uint4(RowType<T>::pack2(o[i] * inv, o[i + 1] * inv),
+                            RowType<T>::pack2(o[i + 2] * inv, o[i + 3] * inv),
+                            RowType<T>::pack2(o[i + 4] * inv, o[i + 5] * inv),
+                            RowType<T>::pack2(o[i + 6] * inv, o[i + 7] * inv));
+  if (a.lse && d == 0) a.lse[row * a.q_heads + head] = row_lse(m, l);
 }
 
 }  // namespace at
