@@ -76,6 +76,12 @@ int launch_join(void (*kernel)(mk::at::AttnArgs, mk::at::Partials, int, int), di
   return launched();
 }
 
+// What a unit costs besides its key tiles, in key tiles (mk_split.cuh), by sweeps: two
+// for tiles of rows (8 prompts of up to 4096 tokens at head_dim 128: 385 us at 0, 366 at 1,
+// 364 at 2, 377 at 4), two for few rows (64 sequences of up to 4096 over an e4m3 cache:
+// 51.3 us at 0, 50.2 at 1, 49.2 at 2 and more).
+constexpr int kFewExtra = 2, kFlashExtra = 2;
+
 template <class T, class C, int HD, int NT>
 int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
   using F = mk::at::FewCfg<C, HD, NT>;
@@ -93,7 +99,7 @@ int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream
   while (mk::at::partial_bytes(ctas, F::ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
   const mk::at::Partials p = mk::at::carve(ws, ctas, F::ROWS, HD);
   const int tq = F::ROWS / a.group;
-  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, 1);
+  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, kFewExtra, 1);
   const int rc = launched();
   const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
   return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);
@@ -154,6 +160,7 @@ int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStre
   mk::at::FlashArgs fa;
   fa.a = a;
   fa.tq1 = 128 / a.group;
+  fa.extra = kFlashExtra;
   fa.least = 1;
   fa.box_shift = 7;
   if (!encode_map(&fa.q, a.q, BF, HD, a.group, a.rows, a.kv_heads, a.q_hs, a.q_ts,

@@ -7,14 +7,12 @@
 // takes half of tensor memory and one row tile has two score buffers.
 //
 //   S = Q K^T   both from shared memory, 128 x 128 fp32 into TMEM
-//   P = 2^(S c - m)  by a warpgroup, a thread for each row: scores from TMEM,
-//                    weights back as 16-bit pairs over the scores' columns
+//   P = 2^(S c - m)  by two warpgroups, one or two threads for each row: scores from
+//                    TMEM, weights back as 16-bit pairs over the scores' columns
 //   O += P V    P from TMEM, V as it lies in memory (MN-major)
 //
-// Warps: one TMA producer, one MMA issuer, a softmax warpgroup for each
-// stream (one at head_dim 256).  While a warpgroup works on one tile, the
-// tensor cores run the other stream's products (or the next tile's scores and
-// the last one's output).  The maximum of a row is raised only when a score
+// Warps: one TMA producer, two MMA issuers, two softmax warpgroups.  While these work on one tile, the tensor cores run the other stream's
+// products (or the next tile's scores and the last one's output).  The maximum of a row is raised only when a score
 // passes it by far (mk_paged.cuh, Weights), and only then is O rescaled in TMEM;
 // the sum of weights is kept in fp32 from the unrounded weights.
 //
@@ -38,6 +36,19 @@ namespace at {
 constexpr int KEYS = 128;  // keys of a tile
 constexpr long long FLASH_WAIT_NS = 2000000000LL;
 
+template <int NQ>
+struct FlashBars {
+  uint64_t q_full, q_ready, q_empty;
+  uint64_t full[2][8], empty[8];  // full: of keys, of values
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t sc_full[8];
+  uint32_t tmem;
+  int gave_up;
+  int per;
+  Cursor<KEYS> start;
+  float trade[2][2][NQ == 1 ? 128 : 1];  // one stream: maxima and sums of a row's two halves
+};
+
 template <class C, int HD>
 struct FlashCfg {
   static constexpr bool E8 = __is_same(C, E4m3);
@@ -50,15 +61,21 @@ struct FlashCfg {
   static constexpr int Q_TILE = 128 * HD * 2;
   static constexpr int STAGES = HD == 64 ? 8 : E8 ? 4 : 5;
   static constexpr int SCALES = E8 ? 8 : 0;  // tiles whose scales are kept
-  static constexpr int SOFT_WARPS = 4 * NQ;
+  // Two softmax warpgroups: one for each of two streams, or half of every tile's keys
+  // each for one.
+  static constexpr int HALVES = 2 / NQ, COLS = KEYS / HALVES, SOFT_WARPS = 8;
   static constexpr int THREADS = 128 + SOFT_WARPS * 32 + (E8 ? 128 : 0);
-  static constexpr size_t SMEM = 1024 + size_t(NQ) * Q_TILE + size_t(STAGES) * STAGE +
-                                 size_t(SCALES) * 3 * KEYS * 4 + (E8 ? 4 * NQ * 128 * 4 : 0);
-  // registers of a thread: launched with, softmax, the others
-  static constexpr int REGS_SOFT = THREADS == 512 ? 200 : THREADS == 384 ? (NQ == 2 ? 216 : 232) : 0;
-  static constexpr int REGS_REST = THREADS == 512 ? 56 : THREADS == 384 ? (NQ == 2 ? 72 : 136) : 0;
+  static constexpr size_t SMEM = size_t(NQ) * Q_TILE + size_t(STAGES) * STAGE +
+                                 size_t(SCALES) * 3 * KEYS * 4 + (E8 ? 4 * NQ * 128 * 4 : 0) +
+                                 sizeof(FlashBars<NQ>);
+  static_assert(SMEM <= 227 * 1024, "more shared memory than a block can have");
+  // registers of a thread at launch, of softmax and of the others
+  static constexpr int REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int REGS_REST = THREADS == 384 ? 72 : 56;
+  static constexpr int REGS_SOFT =
+      (REGS * THREADS - REGS_REST * (THREADS - SOFT_WARPS * 32)) / (SOFT_WARPS * 32) / 8 * 8;
   static_assert(REGS_SOFT * SOFT_WARPS * 32 + REGS_REST * (THREADS - SOFT_WARPS * 32) <=
-                    (65536 / THREADS / 8 * 8) * THREADS,
+                    REGS * THREADS,
                 "the shares exceed what the block is launched with");
 };
 // A place in the ring of stages.  Keys and values share the ring but not the
@@ -97,29 +114,18 @@ struct FlashArgs {
   CUtensorMap q, k, v;  // q: (dim, head of the group, row, key head); k, v: (dim, position, head, page)
   int tq1;              // tokens of a row tile
   int box_shift;        // log2 of the positions of a K box
-  int least;
-};
-
-struct FlashBars {
-  uint64_t q_full, q_ready, q_empty;
-  uint64_t full[2][8], empty[8];  // full: of keys, of values
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t sc_full[8];
-  uint32_t tmem;
-  int gave_up;
-  int per;
-  Cursor<KEYS> start;
+  int extra, least;     // of the line (mk_split.cuh)
 };
 
 // Called by whole warps; the answer is the same in every lane.
-__device__ __forceinline__ bool flash_wait(uint64_t* bar, uint32_t parity, FlashBars* f) {
+__device__ __forceinline__ bool flash_wait(uint64_t* bar, uint32_t parity, int* gave_up) {
   bool ok = true;
   uint64_t start = 0;
   while (!mbar_try_wait(bar, parity)) {
     const uint64_t now = global_ns();
     if (start == 0) start = now;
-    if (now - start > uint64_t(FLASH_WAIT_NS) || *(volatile int*)&f->gave_up) {
-      *(volatile int*)&f->gave_up = 1;
+    if (now - start > uint64_t(FLASH_WAIT_NS) || *(volatile int*)gave_up) {
+      *(volatile int*)gave_up = 1;
       ok = false;
       break;
     }
@@ -138,7 +144,14 @@ __device__ __forceinline__ void make_uniform(Cursor<KEYS>& c) {
   c.j = uniform(c.j);
   c.n = uniform(c.n);
   c.nq = uniform(c.nq);
+  c.at = uniform(c.at);
   c.left = uniform(c.left);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // 32 bytes of a row: one access where the address allows it (rows start on 16).
@@ -180,20 +193,22 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   using F = FlashCfg<C, HD>;
   constexpr bool E8 = F::E8, BF = !E8 && __is_same(T, Bf16);
   constexpr bool RESCALE_Q = E8 && __is_same(T, Bf16);
+  constexpr int HALVES = F::HALVES, COLS = F::COLS;
   constexpr int NQ = F::NQ, STAGES = F::STAGES, PARTS = F::PARTS, CHUNKS = F::CHUNKS;
   using M = typename std::conditional<E8, Fp16, T>::type;
   const AttnArgs& a = fa.a;
-  extern __shared__ unsigned char smem_raw[];
-  __shared__ FlashBars f;
-  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  unsigned char* base_ptr = smem_raw + (base - smem_addr(smem_raw));
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = smem_addr(smem);
+  unsigned char* base_ptr = smem;
   const uint32_t sq = base, ring = base + NQ * F::Q_TILE;
   float* scales = reinterpret_cast<float*>(base_ptr + NQ * F::Q_TILE + STAGES * F::STAGE);
   // sizes of the queries' rows, [4][NQ * 128]: with one stream the scores of two more
   // segments may come before the softmax of one reads them
   float* q_size = scales + F::SCALES * 3 * KEYS;
+  FlashBars<NQ>& f =
+      *reinterpret_cast<FlashBars<NQ>*>(q_size + (E8 ? 4 * NQ * 128 : 0));
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  const Line<KEYS> line{a, NQ * fa.tq1};
+  const Line<KEYS> line{a, NQ * fa.tq1, fa.extra};
   const int tq1 = fa.tq1, tile_rows = tq1 * a.group;
 
   if (warp == 0) {
@@ -220,9 +235,9 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&f.s_full[i], 1);
-      mbar_init(&f.p_full[i], 4);
+      mbar_init(&f.p_full[i], F::SOFT_WARPS / NQ);
       mbar_init(&f.o_full[i], 1);
-      mbar_init(&f.o_empty[i], 4);
+      mbar_init(&f.o_empty[i], F::SOFT_WARPS / NQ);
     }
     fence_barrier_init();
   } else if (warp == 3 && lane == 0) {
@@ -262,8 +277,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     Ring<STAGES> to;
     int seg_no = 0;
     while (at.left > 0) {
-      const int seg = at.segment(), ns = streams(at);
-      bool ok = seg_no == 0 || flash_wait(&f.q_empty, (seg_no - 1) & 1, &f);
+      const int seg = at.segment(line), ns = streams(at);
+      bool ok = seg_no == 0 || flash_wait(&f.q_empty, (seg_no - 1) & 1, &f.gave_up);
       if (!ok) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
@@ -292,7 +307,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           for (int p = 0; p < PARTS; ++p, to.next()) {
             const int st = to.stage;
             // (a fresh barrier's phase before the first counts as complete)
-            if (!flash_wait(&f.empty[st], to.lap ^ 1, &f)) return false;
+            if (!flash_wait(&f.empty[st], to.lap ^ 1, &f.gave_up)) return false;
             to.flip(v);
             uint64_t* full = &f.full[v][st];
             const int rows = v && F::VK < (1 << shift) ? F::VK : 1 << shift;  // of a box
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
       ++seg_no;
     }
     // copies in flight must land before the CTA can end
-    if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f);
+    if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f.gave_up);
     if (!E8)
       for (int i = 0; i < STAGES; ++i)
         for (int v = 0; v < 2; ++v) {  // the last load of each kind (of none: complete at once)
@@ -362,13 +377,15 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
             tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, p + c + k > 0);
       }
     };
+    // the weights lie over the scores, those of a half over its own
+    auto weights_at = [](int key) { return key / 2 + (HALVES == 2 && key >= 64 ? 32 : 0); };
     auto issue_o = [&](int slot, int s, int st, bool more) {
 #pragma unroll
       for (int p = 0; p < PARTS; ++p, st = on(st)) {
         const uint64_t vd = desc_mn_major(ring + st * F::STAGE, F::VK * 128);
 #pragma unroll
         for (int k = 0; k < F::VK / 16; ++k)
-          tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + (p * F::VK + k * 16) / 2,
+          tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + weights_at(p * F::VK + k * 16),
                     vd + k * (2048 / 16), id_o, more || p + k > 0);
       }
     };
@@ -378,7 +395,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
       bool ok = true;
 #pragma unroll
       for (int p = 0; p < PARTS; ++p, ring_at.next())
-        ok = ok && flash_wait(&f.full[v][ring_at.stage], ring_at.flip(v), &f);
+        ok = ok && flash_wait(&f.full[v][ring_at.stage], ring_at.flip(v), &f.gave_up);
       return ok;
     };
     auto pass = [&] {
@@ -410,11 +427,11 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     };
     bool ok = true;
     while (at.left > 0 && ok) {
-      const int seg = at.segment(), end = at.j + seg, ns = streams(at);
+      const int seg = at.segment(line), end = at.j + seg, ns = streams(at);
       // (whoever issues scores; the outputs' issuer of one stream may be two segments
       // behind, where the barrier's parity says nothing)
       if (NQ == 2 || me == 0)
-        ok = flash_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f);
+        ok = flash_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f.gave_up);
       int k_at, v_at;
       if constexpr (NQ == 2) {
         const bool active = me < ns;
@@ -437,8 +454,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           if (j < e) {
             clear_tail(v_at, j);
             // O is free once the epilogue of the stream's last segment has read it
-            if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f);
-            ok = ok && flash_wait(&f.p_full[me], cnt & 1, &f);
+            if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
+            ok = ok && flash_wait(&f.p_full[me], cnt & 1, &f.gave_up);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -466,14 +483,14 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         }
         if (active) {
           // a stream without tiles here keeps step with its epilogues all the same
-          if (ok && e <= at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f);
+          if (ok && e <= at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
           ++segs;
         }
       } else if (me == 0) {
         for (int x = 0; x < seg && ok; ++x, ++cnt) {
           ok = take(0, k_at);
           // the scores' columns are free once the output has used the weights in them
-          if (ok && cnt > 1) ok = flash_wait(&f.o_full[cnt & 1], ((cnt >> 1) - 1) & 1, &f);
+          if (ok && cnt > 1) ok = flash_wait(&f.o_full[cnt & 1], ((cnt >> 1) - 1) & 1, &f.gave_up);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -492,8 +509,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           ok = take(1, v_at);
           if (!ok) break;
           clear_tail(v_at, j);
-          if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[0], (segs - 1) & 1, &f);
-          ok = ok && flash_wait(&f.p_full[cnt & 1], (cnt >> 1) & 1, &f);
+          if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[0], (segs - 1) & 1, &f.gave_up);
+          ok = ok && flash_wait(&f.p_full[cnt & 1], (cnt >> 1) & 1, &f.gave_up);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -511,20 +528,39 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     __syncwarp();
   }
   } else if (warp < 4 + F::SOFT_WARPS) {
-    // ---- softmax and epilogue: a thread for each row of stream s
+    // ---- softmax and epilogue.  Two streams: a thread for each row of its warpgroup's
+    // stream.  (Two threads a row, 64 keys each, made the streams run in step, both at
+    // the exponential unit and then both at the tensor cores: 4450 cycles a key
+    // tile at head_dim 128 where this takes 3140.)  One stream: two threads a row, which halves
+    // the time from scores to weights and the epilogue (2300 cycles a key tile, 2560 with
+    // one).
     more_registers<F::REGS_SOFT>();
-    const int s = (warp - 4) >> 2, r = tid & 127, quarter = warp & 3;
+    const int group = (warp - 4) >> 2, quarter = warp & 3;
+    const int s = NQ == 2 ? group : 0, half = NQ == 2 ? 0 : group;
+    const int r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
     int cnt = 0, seg_no = 0, tiles = 0;  // own key tiles, segments, all key tiles so far
+    uint32_t turn = 0;                   // buffer of the next trade
+    // The other half's number for this row; the two warps meet at their own barrier.
+    // Every warp makes every trade, also after a wait that ran out: they meet as often.
+    // (The buffers alternate: a trade's number is read before the next but one, which
+    // follows another meeting.)
+    auto trade = [&](float x) {
+      f.trade[turn][half][r] = x;
+      named_sync(1 + quarter, 64);
+      const float y = f.trade[turn][half ^ 1][r];
+      turn ^= 1;
+      return y;
+    };
     // The output through key tile x.  Its barrier goes by the score buffer: with one
     // stream the scores of tile x + 1 come before the output of tile x, so that two
     // outputs may be due at once, and one barrier's parity could not tell them apart.
     auto wait_output = [&](int x) {
-      return flash_wait(&f.o_full[NQ == 1 ? x & 1 : s], (NQ == 1 ? x >> 1 : x) & 1, &f);
+      return flash_wait(&f.o_full[NQ == 1 ? x & 1 : s], (NQ == 1 ? x >> 1 : x) & 1, &f.gave_up);
     };
     while (at.left > 0) {
       const Cursor<KEYS> u = at;
-      const int seg = u.segment(), end = u.j + seg;
+      const int seg = u.segment(line), end = u.j + seg;
       at.skip(line, seg);
       make_uniform(at);
       const int seg_at = seg_no++, tile0 = tiles - u.j;
@@ -539,50 +575,67 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
       float m = -INFINITY, l0 = 0.f, l1 = 0.f;  // m in powers of two
       float c = a.scale_log2;
       bool ok = true;
-      for (int j = u.j; j < e && ok; ++j, ++cnt) {
+      for (int j = u.j; j < e; ++j, ++cnt) {
         const int slot = NQ == 1 ? cnt & 1 : s;
-        const uint32_t scores = lanes + slot * KEYS;
-        const float* sc = scales + ((tile0 + j) & 7) * 3 * KEYS;
-        ok = flash_wait(&f.s_full[slot], (NQ == 1 ? cnt >> 1 : cnt) & 1, &f);
-        if constexpr (E8) ok = ok && flash_wait(&f.sc_full[(tile0 + j) & 7], (tile0 + j) >> 3 & 1, &f);
+        const uint32_t scores = lanes + slot * KEYS + half * COLS;
+        const float* sc = scales + ((tile0 + j) & 7) * 3 * KEYS + half * COLS;
+        ok = ok && flash_wait(&f.s_full[slot], (NQ == 1 ? cnt >> 1 : cnt) & 1, &f.gave_up);
+        if constexpr (E8)
+          ok = ok && flash_wait(&f.sc_full[(tile0 + j) & 7], (tile0 + j) >> 3 & 1, &f.gave_up);
         // (the converters wrote it before the first tile's scales)
         if (RESCALE_Q && j == u.j)
           c = a.scale_log2 * q_size[(seg_at & 3) * NQ * 128 + s * 128 + r];
-        if (!ok) break;
-        tc_fence_after();
         if (any_live) {
-          float x[KEYS];
+          // 16-bit caches keep the scores in registers; with an e4m3 cache's scales in the
+          // way they are fetched from TMEM again, 32 at a time, for the weights.
+          constexpr int HELD = E8 ? 32 : COLS;
+          float x[HELD];
+          const int keep = limit - j * KEYS - half * COLS;
+          const bool masked = j * KEYS + KEYS > sure;
+          auto fetch = [&](int from) {
+            if (ok) {
+              tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < KEYS; i += 32) tmem_ld32(scores + i, x + i);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < KEYS; ++i) pin(x[i]);
-          if constexpr (E8) {
-#pragma unroll
-            for (int i = 0; i < KEYS; i += 4) {
-              const float4 kc = *reinterpret_cast<const float4*>(sc + i);
-              const float4 vl = *reinterpret_cast<const float4*>(sc + KEYS + i);
-              x[i] = fmaf(x[i] * c, kc.x, vl.x);
-              x[i + 1] = fmaf(x[i + 1] * c, kc.y, vl.y);
-              x[i + 2] = fmaf(x[i + 2] * c, kc.z, vl.z);
-              x[i + 3] = fmaf(x[i + 3] * c, kc.w, vl.w);
+              for (int i = 0; i < HELD; i += 32) tmem_ld32(scores + from + i, x + i);
+              tmem_wait_ld();
             }
-          }
-          if (j * KEYS + KEYS > sure) {
-            const int keep = limit - j * KEYS;
 #pragma unroll
-            for (int i = 0; i < KEYS; ++i) x[i] = i < keep ? x[i] : -INFINITY;
-          }
-          float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+            for (int i = 0; i < HELD; ++i) pin(x[i]);
+            if constexpr (E8) {
 #pragma unroll
-          for (int i = 4; i < KEYS; i += 4) {
-            t0 = fmaxf(t0, x[i]);
-            t1 = fmaxf(t1, x[i + 1]);
-            t2 = fmaxf(t2, x[i + 2]);
-            t3 = fmaxf(t3, x[i + 3]);
+              for (int i = 0; i < HELD; i += 4) {
+                const float4 kc = *reinterpret_cast<const float4*>(sc + from + i);
+                const float4 vl = *reinterpret_cast<const float4*>(sc + KEYS + from + i);
+                x[i] = fmaf(x[i] * c, kc.x, vl.x);
+                x[i + 1] = fmaf(x[i + 1] * c, kc.y, vl.y);
+                x[i + 2] = fmaf(x[i + 2] * c, kc.z, vl.z);
+                x[i + 3] = fmaf(x[i + 3] * c, kc.w, vl.w);
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < HELD; ++i) x[i] = from + i < keep ? x[i] : -INFINITY;
+            }
+          };
+          auto largest = [&](float t0) {
+            float t1 = x[0];
+#pragma unroll
+            for (int i = 1; i + 3 < HELD; i += 4) {
+              t0 = max3(t0, x[i], x[i + 1]);
+              t1 = max3(t1, x[i + 2], x[i + 3]);
+            }
+            t0 = max3(t0, x[HELD - 3], x[HELD - 2]);
+            return max3(t0, t1, x[HELD - 1]);
+          };
+          float t0 = -INFINITY;
+#pragma unroll
+          for (int from = 0; from < COLS; from += HELD) {
+            fetch(from);
+            t0 = largest(t0);
           }
           const float unit = E8 ? 1.f : c;
-          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * unit;
+          float top = t0 * unit;
+          if (HALVES == 2) top = fmaxf(top, trade(top));
           const bool rise = top > m + Weights<M>::RAISE;
           if (__any_sync(0xffffffffu, rise)) {
             const float up = rise ? top - Weights<M>::LIFT : m;
@@ -591,12 +644,11 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
             l1 *= fac;
             m = up;
             if (j > u.j) {
-              // the last tile's output is complete; scale it
-              ok = wait_output(cnt - 1);
-              if (!ok) break;
+              // the last tile's output is complete; scale this half of its columns
+              ok = ok && wait_output(cnt - 1);
               tc_fence_after();
 #pragma unroll 1
-              for (int d = 0; d < HD; d += 32) {
+              for (int d = half * (HD / HALVES); ok && d < (half + 1) * (HD / HALVES); d += 32) {
                 float o[32];
                 tmem_ld32(lanes + 256 + s * HD + d, o);
                 tmem_wait_ld();
@@ -611,12 +663,14 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           }
           const float off = m == -INFINITY ? 0.f : -m;
           const float* vi = sc + 2 * KEYS;
+          uint32_t held[E8 ? COLS / 2 : 1];
 #pragma unroll
-          for (int i = 0; i < KEYS; i += 32) {
+          for (int i = 0; i < COLS; i += 32) {
             uint32_t p[16];
+            if (HELD == 32) fetch(i);
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
-              float &p0 = x[i + y], &p1 = x[i + y + 1];
+              float &p0 = x[i % HELD + y], &p1 = x[i % HELD + y + 1];
               fma2(p0, p1, unit, off);
               p0 = ex2(p0);
               p1 = ex2(p1);
@@ -629,74 +683,84 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
               }
               p[y / 2] = RowType<M>::pack2(p0, p1);
             }
-            tmem_st16(scores + i / 2, p);
+            if (HELD == 32) {
+              // (they go over scores that are still to be fetched)
+#pragma unroll
+              for (int y = 0; y < 16; ++y) held[i / 2 + y] = p[y];
+            } else if (ok) {
+              tmem_st16(scores + i / 2, p);
+            }
+          }
+          if (HELD == 32 && ok) {
+#pragma unroll
+            for (int i = 0; i < COLS / 2; i += 16) tmem_st16(scores + i, held + i);
           }
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&f.p_full[slot]);
+        if (ok && lane == 0) mbar_arrive(&f.p_full[slot]);
       }
       // ---- epilogue
       if (ok && e > u.j) ok = wait_output(cnt - 1);
       tc_fence_after();
       const bool whole = u.j == 0 && seg == u.n;
       float l = l0 + l1;
-      if (!ok) l = m = __int_as_float(0x7FC00000);  // a wait ran out: NaN
+      if (HALVES == 2) l += trade(l);
+      if (!ok || *(volatile int*)&f.gave_up) {
+        ok = false;
+        l = m = __int_as_float(0x7FC00000);  // a wait ran out: NaN
+      }
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int head = u.h * a.group + r % a.group;
       const long long row = u.s.first + (live ? token : 0);
       const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
       const int part_row = s * tile_rows + r;
       if (any_live) {
-        // A thread has its row, 32 columns at a time.  A finished row leaves in whole
-        // 32-byte sectors; partial rows lie side by side, [column / 4][row] float4, so that
-        // a warp's store is 512 bytes in a piece.  (Trading values between lanes until rows
-        // leave in 64-byte pieces took 4900 cycles a segment at head_dim 128, all of it
+        // A thread has its row (or half of it), 32 columns at a time.  A finished row leaves in
+        // whole 32-byte sectors; partial rows lie side by side, [column / 4][row] float4, so
+        // that a warp's store is 512 bytes in a piece.  (Trading values between lanes until
+        // rows leave in 64-byte pieces took 4900 cycles a segment at head_dim 128, all of it
         // instructions; 16 bytes a lane straight to rows of fp32 10000.)
         const bool none = e <= u.j;  // no tiles here: O is not this segment's
         unsigned char* out = a.out + (row * a.o_ts + head * a.o_hs) * 2;
         float4* pieces = reinterpret_cast<float4*>(part.o) +
                          slot * (HD / 4) * (NQ * 128) + part_row;
+        const int d0 = half * (HD / HALVES);
         float o[32];
-        tmem_ld32(lanes + 256 + s * HD, o);
+        tmem_ld32(lanes + 256 + s * HD + d0, o);
 #pragma unroll 1
-        for (int d = 0; d < HD; d += 32) {
-          float v[32];
+        for (int d = d0; d < d0 + HD / HALVES; d += 32) {
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             pin(o[i]);
-            v[i] = o[i];
+            if (none || !ok) o[i] = ok ? 0.f : l;
           }
-          if (d + 32 < HD) tmem_ld32(lanes + 256 + s * HD + d + 32, o);
-          if (none || !ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ok ? 0.f : l;
-          }
-          if (!live) continue;
-          if (whole) {
+          if (live && whole) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              mul2(v[i], v[i + 1], inv, inv);
-              w[i / 2] = RowType<T>::pack2(v[i], v[i + 1]);
+              mul2(o[i], o[i + 1], inv, inv);
+              w[i / 2] = RowType<T>::pack2(o[i], o[i + 1]);
             }
             store32(out + d * 2, w);
             store32(out + d * 2 + 32, w + 8);
-          } else {
+          } else if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              pieces[(d + i) / 4 * (NQ * 128)] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              pieces[(d + i) / 4 * (NQ * 128)] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
+          if (d + 32 < d0 + HD / HALVES) tmem_ld32(lanes + 256 + s * HD + d + 32, o);
         }
-        if (live && whole) {
-          if (a.lse) a.lse[row * a.q_heads + head] = row_lse(m, l);
-        } else if (live) {
-          part.ml[slot * (NQ * 128) + part_row] = make_float2(m, l);
+        if (live && half == 0) {
+          if (!whole)
+            part.ml[slot * (NQ * 128) + part_row] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[row * a.q_heads + head] = row_lse(m, l);
         }
       }
-      if (s == 0 && r == 0 && u.j == 0 && !whole) {
+      if (s == 0 && half == 0 && r == 0 && u.j == 0 && !whole) {
         Left left = {u.b, u.h, u.i, (u.n - seg + f.per - 1) / f.per};
         part.left[blockIdx.x] = left;
       }
@@ -711,10 +775,10 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
     constexpr int N = F::STAGE / 32 / 128;  // 16-code pieces of a thread and stage
     int it = 0, seg_no = 0, tiles = 0;
     while (at.left > 0) {
-      const int seg = at.segment(), end = at.j + seg, ns = streams(at);
+      const int seg = at.segment(line), end = at.j + seg, ns = streams(at);
       bool ok = true;
       if constexpr (RESCALE_Q) {
-        ok = flash_wait(&f.q_full, seg_no & 1, &f);
+        ok = flash_wait(&f.q_full, seg_no & 1, &f.gave_up);
         if (!ok) break;
         for (int s = 0; s < ns; ++s) {
           const uint32_t row = sq + s * F::Q_TILE + ct * 128;
@@ -814,7 +878,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         }
         if (n + 1 < 2 * seg * PARTS) load(n + 1, next);
         const int st = it % STAGES;
-        ok = it < STAGES || flash_wait(&f.empty[st], (it / STAGES - 1) & 1, &f);
+        ok = it < STAGES || flash_wait(&f.empty[st], (it / STAGES - 1) & 1, &f.gave_up);
         if (!ok) break;
         const int rows = v ? F::VK : KEYS;
 #pragma unroll

@@ -127,7 +127,7 @@ __device__ __forceinline__ uint32_t piece(int r, int ch) {
 
 template <class T, class C, int HD, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
-    attn_few_kernel(const __grid_constant__ AttnArgs a, Partials part, int tq, int least) {
+    attn_few_kernel(const __grid_constant__ AttnArgs a, Partials part, int tq, int extra, int least) {
   using F = FewCfg<C, HD, NT>;
   constexpr bool E8 = F::E8;
   using M = typename std::conditional<E8, Fp16, T>::type;  // what the products multiply
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   __shared__ long long s_per;
   __shared__ Cursor<FEW_KEYS> s_cursor;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Line<FEW_KEYS> line{a, tq};
+  const Line<FEW_KEYS> line{a, tq, extra};
   if (warp == 0) {
     long long per;
     const Cursor<FEW_KEYS> c = find_share<FEW_KEYS>(line, blockIdx.x, gridDim.x, least, per);
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   while (at.left > 0) {
     // ---- one segment: the tiles of one unit that lie in this share
     const Cursor<FEW_KEYS> u = at;
-    const int seg = u.segment();
+    const int seg = u.segment(line);
     // queries: row r is token r / group of the tile, head r % group
     uint32_t q[NT][STEPS][2];
     float qs[NT][2];

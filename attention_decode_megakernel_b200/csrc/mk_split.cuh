@@ -5,11 +5,15 @@
 // consecutive new tokens times the `group` query heads that share the head.
 // It walks ceil(limit / KT) tiles of KT keys, where limit is what its last
 // token sees (one tile at least, so that rows without keys are written too).
-// All tiles of all units, ordered by sequence, head, row tile and key tile,
-// form one line, and CTA c takes the tiles [c * per, (c + 1) * per) of it:
-// every CTA gets the same number of key tiles whatever the lengths, for one
-// long sequence as for a ragged batch.  A unit that lies in one CTA's share
-// is finished there.  A unit that crosses shares leaves a partial {sum of
+// All units, ordered by sequence, head and row tile, form one line, each as
+// long as its key tiles and `extra` more for what a unit costs besides them
+// (queries, first scores, epilogue), and CTA c takes the stretch [c * per,
+// (c + 1) * per) of it: every CTA gets the same work whatever the lengths, for
+// one long sequence as for a ragged batch.  (Without the extra length, CTAs
+// among the short units at the front of a prompt took 1.7 times as long as the
+// others.)  Key tile j of a unit lies at extra + j; a stretch that ends before the first
+// one leaves the unit to the next CTA.  A unit that lies in one CTA's share is
+// finished there.  A unit that crosses shares leaves a partial {sum of
 // weighted values, maximum, sum of weights} in each CTA (a CTA has at most
 // two: slot 2c for the unit it entered in the middle, 2c + 1 for the one it
 // left), and join_kernel adds them in the order of the CTAs: no atomics, the
@@ -65,7 +69,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
 template <int KT>
 struct Line {
   const AttnArgs& a;
-  int tq;
+  int tq, extra;
 
   __device__ int row_tiles(const Seq& s) const { return (s.n_new + tq - 1) / tq; }
   // keys that the last token of row tile i sees (may be negative)
@@ -88,11 +92,13 @@ struct Line {
       return none + floor_sum<unsigned>(unsigned(n), KT, unsigned(tq), unsigned(b));
     return none + floor_sum<unsigned long long>(n, KT, tq, b);
   }
-  // key tiles of one head of the sequence
+  // the length of the first x row tiles, and of one head of the sequence
+  __device__ long long length(const Seq& s, int x) const {
+    return x ? before(s, x) + (long long)x * extra : 0;
+  }
   __device__ long long all(const Seq& s) const {
     const int nq = row_tiles(s);
-    if (nq == 0) return 0;
-    return (nq > 1 ? before(s, nq - 1) : 0) + tiles(s, nq - 1);
+    return nq ? length(s, nq - 1) + tiles(s, nq - 1) + extra : 0;
   }
 };
 
@@ -101,15 +107,24 @@ template <int KT>
 struct Cursor {
   Seq s;
   int b, h, i, j, n, nq;
-  int left;  // tiles of this CTA's share from here on
+  int at;    // place in the unit: 0 .. extra + n
+  int left;  // length of this CTA's share from here on
 
   // tiles of the present unit that lie in this share
-  __device__ int segment() const { return n - j < left ? n - j : left; }
+  __device__ int segment(const Line<KT>& line) const {
+    const int end = at + left - line.extra;
+    return (end < n ? end : n) - j;
+  }
+  // past `tiles` of them; at the unit's end, on to the next unit
   __device__ void skip(const Line<KT>& line, int tiles) {
-    left -= tiles;
     j += tiles;
-    if (j < n || left <= 0) return;
-    j = 0;
+    left -= line.extra + j - at;
+    at = line.extra + j;
+    if (j < n || left <= line.extra) {
+      if (j == n) left = 0;  // the share ends before the next unit's first tile
+      return;
+    }
+    at = j = 0;
     if (++i == nq) {
       i = 0;
       if (++h == line.a.kv_heads) {
@@ -124,8 +139,8 @@ struct Cursor {
   }
 };
 
-// The place and share of CTA `cta` of `ctas`, shares of at least `least`
-// tiles; `per` receives a share's tiles.  Called by one whole warp with all
+// The place and share of CTA `cta` of `ctas`, shares of at least `least`;
+// `per` receives a share's length.  Called by one whole warp with all
 // lanes; the result is the same in every lane.
 template <int KT>
 __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, int ctas,
@@ -175,14 +190,16 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
   int lo = 0, span = c.nq;  // it is one of lo .. lo + span - 1
   while (span > 1) {
     const int step = (span + 31) / 32, x = lo + lane * step;
-    const bool at_or_before = x == 0 || (lane * step < span && line.before(c.s, x) <= off);
+    const bool at_or_before = x == 0 || (lane * step < span && line.length(c.s, x) <= off);
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, at_or_before));
     span = span - last * step < step ? span - last * step : step;
     lo += last * step;
   }
   c.i = lo;
-  c.j = int(off - (lo ? line.before(c.s, lo) : 0));
+  c.at = int(off - line.length(c.s, lo));
+  c.j = c.at > line.extra ? c.at - line.extra : 0;
   c.n = line.tiles(c.s, c.i);
+  if (c.at + c.left <= line.extra) c.left = 0;
   return c;
 }
 
