@@ -82,29 +82,6 @@ int launch_join(void (*kernel)(mk::at::AttnArgs, mk::at::Partials, int, int), di
 // 51.3 us at 0, 50.2 at 1, 49.2 at 2 and more).
 constexpr int kFewExtra = 2, kFlashExtra = 2;
 
-template <class T, class C, int HD, int NT>
-int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
-  using F = mk::at::FewCfg<C, HD, NT>;
-  auto* kernel = &mk::at::attn_few_kernel<T, C, HD, NT>;
-  static bool done[kMaxDevices] = {};
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return MK_ERR_CUDA;
-    }
-    done[dev] = true;
-  }
-  int ctas = sms;
-  while (mk::at::partial_bytes(ctas, F::ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
-  const mk::at::Partials p = mk::at::carve(ws, ctas, F::ROWS, HD);
-  const int tq = F::ROWS / a.group;
-  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(a, p, tq, kFewExtra, 1);
-  const int rc = launched();
-  const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
-  return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);
-}
-
 // cuTensorMapEncodeTiled through the runtime (no link against the driver library).
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -141,6 +118,57 @@ bool encode_map(CUtensorMap* m, const void* base, bool bf16, long long d0, long 
             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A paged cache's rows as boxes of (128 bytes, 16 positions, all columns of 128 bytes):
+// 64-byte rows as one column of 64.
+bool encode_rows(CUtensorMap* m, const void* base, const mk::PagedView& c, int row) {
+  const EncodeFn fn = encode_tiled();
+  if (!fn) return false;
+  const bool e8 = row == c.head_dim;
+  const int size = e8 ? 1 : 2, col = row < 128 ? row : 128;  // bytes
+  const cuuint64_t dims[5] = {cuuint64_t(col / size), cuuint64_t(c.page_size),
+                              cuuint64_t(row / col), cuuint64_t(c.kv_heads),
+                              cuuint64_t(c.n_pages)};
+  auto stride = [&](long long s) { return s > 0 ? cuuint64_t(s) * size : cuuint64_t(16); };
+  const cuuint64_t strides[4] = {stride(c.pos_stride), cuuint64_t(col), stride(c.head_stride),
+                                 stride(c.page_stride)};
+  const cuuint32_t box[5] = {cuuint32_t(col / size), 16u, cuuint32_t(row / col), 1u, 1u};
+  const cuuint32_t step[5] = {1u, 1u, 1u, 1u, 1u};
+  return fn(m, e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, class C, int HD, int NT>
+int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+  using F = mk::at::FewCfg<C, HD, NT>;
+  auto* kernel = &mk::at::attn_few_kernel<T, C, HD, NT>;
+  static bool done[kMaxDevices] = {};
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(F::SMEM)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  int ctas = sms;
+  while (mk::at::partial_bytes(ctas, F::ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
+  const mk::at::Partials p = mk::at::carve(ws, ctas, F::ROWS, HD);
+  const int tq = F::ROWS / a.group;
+  mk::at::FewArgs fa;
+  fa.a = a;
+  fa.tq = tq;
+  fa.extra = kFewExtra;
+  fa.least = 1;
+  if (!encode_rows(&fa.k, a.c.k, a.c, F::ROW) || !encode_rows(&fa.v, a.c.v, a.c, F::ROW))
+    return MK_ERR_UNSUPPORTED;
+  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(fa, p);
+  const int rc = launched();
+  const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
+  return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);
 }
 
 template <class T, class C, int HD, bool PAGED>

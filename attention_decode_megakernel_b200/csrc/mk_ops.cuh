@@ -51,8 +51,8 @@ inline int cache_view(const mk_kv_cache* c, mk::PagedView* v) {
   if (c->pos_stride < c->head_dim || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
       (c->n_pages > 1 && c->page_stride < c->head_dim))
     return MK_ERR_ARG;
-  if (c->dtype == MK_E4M3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) ||
-                              !aligned(c->v_scale, 4)))
+  if (c->dtype == MK_E4M3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) ||
+                              !aligned(c->v_scale, 16)))
     return MK_ERR_ARG;
   v->k = static_cast<unsigned char*>(c->k);
   v->v = static_cast<unsigned char*>(c->v);

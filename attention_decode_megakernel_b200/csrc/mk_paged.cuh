@@ -5,10 +5,12 @@
 // The cache's bytes bound it: every K and V row of a (sequence, key head) is
 // read once, for 2 * 8 * NT multiply-adds a value.  So the layout serves the
 // loads.  Each of the four warps walks its own subtiles of 16 keys through a
-// private ring of stages in shared memory, filled by 16-byte cp.async copies
-// that look up the page, leave out what lies behind the sequence (zeros) and
-// place the pieces so that no read has bank conflicts.  No barrier joins the
-// warps until the unit ends, and the ring runs ahead into the next unit.
+// private ring of stages in shared memory: one lane asks TMA for the 16 rows
+// of K and of V, a box of (128 bytes, 16 positions, columns of 128 bytes) in the
+// 128-byte swizzle, and looks the next page up a step ahead.  (16-byte cp.async copies
+// by all lanes took half of the instructions, and one warp a scheduler is bound
+// by those: 64 sequences over an e4m3 cache took 49 us.)  No barrier joins the warps
+// until the unit ends, and the ring runs ahead into the next unit.
 //
 // The products run on mma.m16n8k16 with the keys as M: S^T = K Q^T and
 // O^T = V^T P^T, so that 8 rows (N) cost 8 columns, not a tile of 128 rows.
@@ -30,6 +32,7 @@
 #include <type_traits>
 
 #include "mk_split.cuh"
+#include "mk_tc.cuh"
 
 namespace mk {
 namespace at {
@@ -37,6 +40,7 @@ namespace at {
 constexpr int FEW_WARPS = 4;
 constexpr int FEW_KEYS = 16 * FEW_WARPS;  // keys of a tile: 16 a warp
 constexpr int FEW_THREADS = 32 * FEW_WARPS;
+constexpr long long FEW_WAIT_NS = 2000000000LL;
 
 // The weight of the score that sets m is 2^LIFT, the largest one 2^RAISE.
 template <class M>
@@ -44,32 +48,48 @@ struct Weights {
   static constexpr float LIFT = __is_same(M, Fp16) ? 7.f : 0.f, RAISE = LIFT + 8.f;
 };
 
+struct FewBars {
+  uint64_t full[FEW_WARPS][8];  // of each warp's stages
+  Cursor<FEW_KEYS> start;
+  int per, gave_up;
+};
+
 template <class C, int HD, int NT>
 struct FewCfg {
   static constexpr bool E8 = __is_same(C, E4m3);
-  static constexpr int ROW = HD * (E8 ? 1 : 2);            // bytes of a cache row
-  static constexpr int STAGE = 32 * ROW + (E8 ? 128 : 0);  // 16 keys, 16 values, their scales
+  static constexpr int ROW = HD * (E8 ? 1 : 2);             // bytes of a cache row
+  static constexpr int STAGE = 32 * ROW + (E8 ? 1024 : 0);  // 16 keys, 16 values; their scales
   static constexpr int ROWS = 8 * NT;
-  static constexpr int JOIN = FEW_WARPS * ROWS * (HD + 4) * 4 + FEW_WARPS * ROWS * 8;
-  static constexpr int FIT = (225 * 1024 - JOIN) / (FEW_WARPS * STAGE);
+  static constexpr int SLOTS = FEW_WARPS / 2;               // of the join: half of the warps at a time
+  static constexpr int JOIN = SLOTS * ROWS * (HD + 4) * 4 + SLOTS * ROWS * 8;
+  static constexpr int FIT = (227 * 1024 - int(sizeof(FewBars)) - JOIN) / (FEW_WARPS * STAGE);
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr size_t SMEM = size_t(FEW_WARPS) * STAGES * STAGE + JOIN;
+  static constexpr size_t SMEM = size_t(FEW_WARPS) * STAGES * STAGE + JOIN + sizeof(FewBars);
   static_assert(STAGES >= 2, "the ring needs two stages");
 };
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
+struct FewArgs {
+  AttnArgs a;
+  CUtensorMap k, v;  // (dim within 128 bytes, position, column of 128 bytes, head, page)
+  int tq, extra, least;
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c1, int c3,
+                                            int c4, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c3), "r"(c4),
+      "r"(smem_addr(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 4 : 0)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 u;
@@ -114,91 +134,124 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Byte offset of 16-byte piece `ch` of row r of a stage whose rows are ROW
-// bytes: the piece's place in its 128-byte line is turned by the row (of two
-// rows to a line: by the line), so that the lanes of every read below (two
-// rows by four pieces, four rows by two pieces, eight rows by one) hit all banks.
+// (relative errors of 2^-22 and less; exact for powers of two)
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Byte offset of 16-byte piece `ch` of row r of 16 rows as TMA lays them down:
+// columns of 128 bytes, the rows of one after another, the piece turned by the
+// row (64-byte rows: by the pair of rows).  Reads of two rows by four pieces then meet
+// twice in a bank, four rows by two pieces and eight rows by one do not.
 template <int ROW>
 __device__ __forceinline__ uint32_t piece(int r, int ch) {
-  const int line = ROW >= 128 ? r : r >> 1;
-  const uint32_t turn = (((line >> 1) & 3) * 2) ^ ((line & 1) * 5);
-  return ((uint32_t(r) * (ROW / 16) + ch) ^ turn) * 16;
+  if constexpr (ROW == 64) return uint32_t(r) * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  return uint32_t(ch >> 3) * 2048 + uint32_t(r) * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
 template <class T, class C, int HD, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
-    attn_few_kernel(const __grid_constant__ AttnArgs a, Partials part, int tq, int extra, int least) {
+    attn_few_kernel(const __grid_constant__ FewArgs fa, Partials part) {
   using F = FewCfg<C, HD, NT>;
   constexpr bool E8 = F::E8;
   using M = typename std::conditional<E8, Fp16, T>::type;  // what the products multiply
   constexpr int ROW = F::ROW, STAGES = F::STAGES, ROWS = F::ROWS;
-  constexpr int STEPS = HD / 16;              // k-steps of a score, m-tiles of the output
+  constexpr int STEPS = HD / 16;               // k-steps of a score, m-tiles of the output
   constexpr int PIECES = HD / (E8 ? 64 : 32);  // 16-byte pieces of a key row a lane reads
+  const AttnArgs& a = fa.a;
+  const int tq = fa.tq;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ long long s_per;
-  __shared__ Cursor<FEW_KEYS> s_cursor;
+  FewBars& f = *reinterpret_cast<FewBars*>(smem + FEW_WARPS * STAGES * F::STAGE + F::JOIN);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Line<FEW_KEYS> line{a, tq, extra};
+  const Line<FEW_KEYS> line{a, tq, fa.extra};
   if (warp == 0) {
     long long per;
-    const Cursor<FEW_KEYS> c = find_share<FEW_KEYS>(line, blockIdx.x, gridDim.x, least, per);
+    const Cursor<FEW_KEYS> c = find_share<FEW_KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
     if (lane == 0) {
-      s_per = per;
-      s_cursor = c;
+      f.per = int(per);
+      f.start = c;
+      f.gave_up = 0;
       Left none = {0, 0, 0, 0};
       part.left[blockIdx.x] = none;
     }
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < FEW_WARPS * 8; ++i) mbar_init(&f.full[0][0] + i, 1);
+    fence_barrier_init();
+  } else if (warp == 2 && lane == 0) {
+    prefetch_map(&fa.k);
+    prefetch_map(&fa.v);
   }
   __syncthreads();
   griddep_launch_dependents();
-  Cursor<FEW_KEYS> at = s_cursor, ahead = at;  // where the math is, where the copies are
+  Cursor<FEW_KEYS> at = f.start, ahead = at;  // where the math is, where the copies are
   if (at.left <= 0) return;
-  const int per = int(s_per);
+  const int per = f.per;
   const uint32_t ring = smem_addr(smem) + warp * (STAGES * F::STAGE);
   unsigned char* join = smem + FEW_WARPS * STAGES * F::STAGE;
-  float* join_o = reinterpret_cast<float*>(join);                       // [warp][ROWS][HD + 4]
-  float2* join_ml = reinterpret_cast<float2*>(join + FEW_WARPS * ROWS * (HD + 4) * 4);
+  float* join_o = reinterpret_cast<float*>(join);  // [slot][ROWS][HD + 4]
+  float2* join_ml = reinterpret_cast<float2*>(join + F::SLOTS * ROWS * (HD + 4) * 4);
 
+  // The page of this warp's keys at `ahead`; n_pages, which lies outside the maps and
+  // arrives as zeros, for one outside the cache.
+  auto page_at = [&] {
+    int page = a.c.n_pages;
+    const int key = ahead.j * FEW_KEYS + warp * 16;
+    if (ahead.left > 0 && key < line.limit(ahead.s, ahead.i))
+      page = a.table[(long long)ahead.b * a.table_stride + (key >> a.c.page_shift)];
+    return page;
+  };
+  uint32_t strange = 0;  // stages whose page lies outside the cache
+  int page = page_at();
   // copies of this warp's 16 keys of the tile at `ahead` into stage st
   auto fetch = [&](int st) {
-    if (ahead.left > 0) {
-      const int key = ahead.j * FEW_KEYS + warp * 16;
-      const int limit = line.limit(ahead.s, ahead.i);
-      if (key < limit) {
-        const int page = a.table[(long long)ahead.b * a.table_stride + (key >> a.c.page_shift)];
-        const bool known = page >= 0 && page < a.c.n_pages;
-        const int off = key & (a.c.page_size - 1);
-        const long long row0 = (known ? page : 0) * a.c.page_stride +
-                               ahead.h * a.c.head_stride + off * a.c.pos_stride;
+    if (ahead.left <= 0) return;
+    const int key = ahead.j * FEW_KEYS + warp * 16;
+    if (key < line.limit(ahead.s, ahead.i)) {
+      const bool known = page >= 0 && page < a.c.n_pages;
+      strange = (strange & ~(1u << st)) | (known ? 0u : 1u << st);
+      if (elect_one()) {
+        const int off = key & (a.c.page_size - 1), p = known ? page : a.c.n_pages;
         const uint32_t dst = ring + st * F::STAGE;
-        constexpr int CH = ROW / 16;                     // pieces of a row
-        constexpr int RPI = CH >= 32 ? 1 : 32 / CH;      // rows a copy of the warp covers
-        const int ch = lane % (CH < 32 ? CH : 32), r0 = lane / (CH < 32 ? CH : 32);
-        constexpr int B = E8 ? 1 : 2;
-#pragma unroll
-        for (int r = 0; r < 16; r += RPI) {
-          const bool take = known && key + r + r0 < limit;
-          const long long src = (row0 + (take ? r + r0 : 0) * a.c.pos_stride) * B + ch * 16;
-          const uint32_t to = dst + piece<ROW>(r + r0, ch);
-          cp_async16_or_zero(to, a.c.k + src, take);
-          cp_async16_or_zero(to + 16 * ROW, a.c.v + src, take);
-        }
-        if constexpr (E8) {
-          const int r = lane & 15;
-          const bool take = known && key + r < limit;
+        uint64_t* bar = &f.full[warp][st];
+        mbar_arrive_expect_tx(bar, 32 * ROW + (E8 && known ? 128 : 0));
+        tma_load_5d(dst, &fa.k, off, ahead.h, p, bar);
+        tma_load_5d(dst + 16 * ROW, &fa.v, off, ahead.h, p, bar);
+        if (E8 && known) {
           const long long sc =
-              (((long long)(known ? page : 0) * a.c.kv_heads + ahead.h) << a.c.page_shift) + off +
-              (take ? r : 0);
-          cp_async4_or_zero(dst + 32 * ROW + lane * 4, (lane < 16 ? a.c.k_scale : a.c.v_scale) + sc,
-                            take);
+              (((long long)page * a.c.kv_heads + ahead.h) << a.c.page_shift) + off;
+          bulk_load(dst + 32 * ROW, a.c.k_scale + sc, 64, bar);
+          bulk_load(dst + 32 * ROW + 64, a.c.v_scale + sc, 64, bar);
         }
       }
-      ahead.skip(line, 1);
+      __syncwarp();
     }
-    cp_async_commit();
+    ahead.skip(line, 1);
+    page = page_at();  // used by the next fetch
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+  uint32_t phases = 0;  // parity of each stage's next load
+  // this stage's load has landed (a wait that runs out: NaN from here on)
+  auto landed = [&](int st) {
+    uint64_t start = 0;
+    while (!mbar_try_wait(&f.full[warp][st], phases >> st & 1)) {
+      const uint64_t now = global_ns();
+      if (start == 0) start = now;
+      if (now - start > uint64_t(FEW_WAIT_NS) || *(volatile int*)&f.gave_up) {
+        *(volatile int*)&f.gave_up = 1;
+        break;
+      }
+    }
+    __syncwarp();
+    phases ^= 1u << st;
+  };
 
   int stage = 0;
   while (at.left > 0) {
@@ -275,12 +328,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
 
     for (int step = 0; step < seg; ++step) {
-      cp_async_wait<STAGES - 2>();
       __syncwarp();
       // the stage of the step before this one, which every lane has left
       fetch(stage == 0 ? STAGES - 1 : stage - 1);
       const int key = (u.j + step) * FEW_KEYS + warp * 16;
       if (key < line.limit(u.s, u.i)) {
+        landed(stage);
+        if (key + 16 > u.s.len) {
+          // what the page holds behind the sequence: weights of 0 would keep its NaN
+          const int keep = u.s.len - key;
+          for (int x = lane; x < (16 - keep) * (ROW / 16); x += 32) {
+            const uint32_t to = ring + stage * F::STAGE + 16 * ROW +
+                                piece<ROW>(keep + x / (ROW / 16), x % (ROW / 16));
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0) : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
         const uint32_t ks = ring + stage * F::STAGE, vs = ks + 16 * ROW;
         float s[NT][4];
 #pragma unroll
@@ -316,9 +380,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           for (int y = 0; y < 2; ++y) {
             kc[y] = __uint_as_float(lds32(vs + 16 * ROW + (g + 8 * y) * 4));
             float sv = __uint_as_float(lds32(vs + 16 * ROW + 64 + (g + 8 * y) * 4));
-            sv = sv > 0.f ? sv : 1.f;  // rows left out
-            vl[y] = log2f(sv);
-            vi[y] = 1.0f / sv;
+            if (strange >> stage & 1) kc[y] = sv = 1.f;  // zeros, whose scales were not read
+            sv = sv > 0.f ? sv : 1.f;                    // behind the sequence: masked
+            vl[y] = lg2(sv);
+            vi[y] = rcp(sv);
           }
         }
         bool rise = false;
@@ -403,7 +468,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       at.skip(line, 1);
     }
 
-    // ---- join the warps and write the segment
+    // ---- join the warps, half of them at a time, and write the segment
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -411,20 +476,57 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 4);
         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 8);
         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 16);
-        const int r = nt * 8 + 2 * t + x;
-        if (g == 0) join_ml[warp * ROWS + r] = make_float2(m[nt][x], l[nt][x]);
-        float* to = join_o + (warp * ROWS + r) * (HD + 4);
+        if (*(volatile int*)&f.gave_up) l[nt][x] = m[nt][x] = __int_as_float(0x7FC00000);
+      }
+    // this lane's values, to slot w
+    auto leave = [&](int w) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          if constexpr (E8) {
-            *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
-                make_float2(o[nt][i][x], o[nt][i][2 + x]);
-          } else {
-            to[16 * i + g] = o[nt][i][x];
-            to[16 * i + 8 + g] = o[nt][i][2 + x];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = nt * 8 + 2 * t + x;
+          if (g == 0) join_ml[w * ROWS + r] = make_float2(m[nt][x], l[nt][x]);
+          float* to = join_o + (w * ROWS + r) * (HD + 4);
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            if constexpr (E8) {
+              *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
+                  make_float2(o[nt][i][x], o[nt][i][2 + x]);
+            } else {
+              to[16 * i + g] = o[nt][i][x];
+              to[16 * i + 8 + g] = o[nt][i][2 + x];
+            }
           }
         }
-      }
+    };
+    if (warp >= F::SLOTS) leave(warp - F::SLOTS);
+    __syncthreads();
+    if (warp < F::SLOTS) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = nt * 8 + 2 * t + x;
+          const float2 ml = join_ml[warp * ROWS + r];
+          const float top = fmaxf(m[nt][x], ml.x), base = top == -INFINITY ? 0.f : top;
+          const float f0 = ex2(m[nt][x] - base), f1 = ex2(ml.x - base);
+          const float* from = join_o + (warp * ROWS + r) * (HD + 4);
+          l[nt][x] = l[nt][x] * f0 + ml.y * f1;
+          m[nt][x] = top;
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            float2 y;
+            if constexpr (E8)
+              y = *reinterpret_cast<const float2*>(from + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
+            else
+              y = make_float2(from[16 * i + g], from[16 * i + 8 + g]);
+            o[nt][i][x] = o[nt][i][x] * f0 + y.x * f1;
+            o[nt][i][2 + x] = o[nt][i][2 + x] * f0 + y.y * f1;
+          }
+        }
+      __syncwarp();
+      leave(warp);
+    }
     __syncthreads();
     const bool whole = u.j == 0 && seg == u.n;
     const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
@@ -433,12 +535,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       if (r >= tq * a.group || token >= u.s.n_new) continue;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < FEW_WARPS; ++w) top = fmaxf(top, join_ml[w * ROWS + r].x);
+      for (int w = 0; w < F::SLOTS; ++w) top = fmaxf(top, join_ml[w * ROWS + r].x);
       const float base = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < FEW_WARPS; ++w) {
+      for (int w = 0; w < F::SLOTS; ++w) {
         const float2 ml = join_ml[w * ROWS + r];
         const float f = ex2(ml.x - base);
         const float4 y = *reinterpret_cast<const float4*>(join_o + (w * ROWS + r) * (HD + 4) + d);
@@ -469,7 +571,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
     __syncthreads();  // the join buffer is free again
   }
-  cp_async_wait<0>();
+  if (*(volatile int*)&f.gave_up)  // copies still on their way land before the CTA ends
+    for (int st = 0; st < STAGES; ++st) {
+      const uint64_t start = global_ns();
+      while (!mbar_try_wait(&f.full[warp][st], (phases >> st & 1) ^ 1))
+        if (global_ns() - start > uint64_t(FEW_WAIT_NS)) break;
+    }
 }
 
 }  // namespace at

@@ -431,8 +431,8 @@ int mk_qk_norm_rope(const mk_rope *rope, const void *q, int64_t q_ts,
  * caller.  The row of (page, head, position) starts page * page_stride +
  * head * head_stride + position * pos_stride values into k and into v, 16-byte
  * aligned; rows do not overlap.  dtype MK_BF16 or MK_FP16, or MK_E4M3 with one
- * float scale for each row in k_scale and v_scale, [page][head][position]
- * without gaps: a row's values are code * scale.  Scales are positive, normal
+ * float scale for each row in k_scale and v_scale (16-byte aligned),
+ * [page][head][position] without gaps: a row's values are code * scale.  Scales are positive, normal
  * numbers; mk_kv_write stores powers of two from 2^-64 to 2^120.  An engine's
  * cache as mk_get_state copies it out is one sequence of such pages (page
  * stride page_size * head_dim, head stride pos * head_dim) when its length is
