@@ -165,7 +165,7 @@ int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream
   fa.least = 1;
   if (!encode_rows(&fa.k, a.c.k, a.c, F::ROW) || !encode_rows(&fa.v, a.c.v, a.c, F::ROW))
     return MK_ERR_UNSUPPORTED;
-  kernel<<<ctas, mk::at::FEW_THREADS, F::SMEM, st>>>(fa, p);
+  kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
   const int rc = launched();
   const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
   return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);

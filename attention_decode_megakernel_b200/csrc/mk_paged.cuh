@@ -4,12 +4,14 @@
 //
 // The cache's bytes bound it: every K and V row of a (sequence, key head) is
 // read once, for 2 * 8 * NT multiply-adds a value.  So the layout serves the
-// loads.  Each of the four warps walks its own subtiles of 16 keys through a
+// loads.  Each of four or eight warps walks its own subtiles of 16 keys through a
 // private ring of stages in shared memory: one lane asks TMA for the 16 rows
 // of K and of V, a box of (128 bytes, 16 positions, columns of 128 bytes) in the
 // 128-byte swizzle, and looks the next page up a step ahead.  (16-byte cp.async copies
-// by all lanes took half of the instructions, and one warp a scheduler is bound
-// by those: 64 sequences over an e4m3 cache took 49 us.)  No barrier joins the warps
+// by all lanes were a quarter of the instructions.)  A warp is bound by the latency of its
+// instructions, four cycles each, so rows of up to 256 bytes, whose stages leave room,
+// have eight warps (64 sequences over an e4m3 cache at head_dim 256: 49 us with
+// four); rows of 512 bytes have four.  No barrier joins the warps
 // until the unit ends, and the ring runs ahead into the next unit.
 //
 // The products run on mma.m16n8k16 with the keys as M: S^T = K Q^T and
@@ -37,9 +39,6 @@
 namespace mk {
 namespace at {
 
-constexpr int FEW_WARPS = 4;
-constexpr int FEW_KEYS = 16 * FEW_WARPS;  // keys of a tile: 16 a warp
-constexpr int FEW_THREADS = 32 * FEW_WARPS;
 constexpr long long FEW_WAIT_NS = 2000000000LL;
 
 // The weight of the score that sets m is 2^LIFT, the largest one 2^RAISE.
@@ -48,23 +47,29 @@ struct Weights {
   static constexpr float LIFT = __is_same(M, Fp16) ? 7.f : 0.f, RAISE = LIFT + 8.f;
 };
 
+template <int WARPS>
 struct FewBars {
-  uint64_t full[FEW_WARPS][8];  // of each warp's stages
-  Cursor<FEW_KEYS> start;
+  uint64_t full[WARPS][8];  // of each warp's stages
+  Cursor<16 * WARPS> start;
   int per, gave_up;
 };
 
 template <class C, int HD, int NT>
 struct FewCfg {
   static constexpr bool E8 = __is_same(C, E4m3);
-  static constexpr int ROW = HD * (E8 ? 1 : 2);             // bytes of a cache row
-  static constexpr int STAGE = 32 * ROW + (E8 ? 1024 : 0);  // 16 keys, 16 values; their scales
+  static constexpr int ROW = HD * (E8 ? 1 : 2);  // bytes of a cache row
+  static constexpr int WARPS = ROW <= 256 ? 8 : 4, THREADS = 32 * WARPS;
+  static constexpr int KEYS = 16 * WARPS;        // of a tile: 16 a warp
+  static constexpr int STAGE = 32 * ROW, SCALES = E8 ? 128 : 0;  // 16 keys, 16 values; their scales
   static constexpr int ROWS = 8 * NT;
-  static constexpr int SLOTS = FEW_WARPS / 2;               // of the join: half of the warps at a time
+  static constexpr int SLOTS = WARPS == 8 ? 3 : 2;  // of the join: so many warps at a time
   static constexpr int JOIN = SLOTS * ROWS * (HD + 4) * 4 + SLOTS * ROWS * 8;
-  static constexpr int FIT = (227 * 1024 - int(sizeof(FewBars)) - JOIN) / (FEW_WARPS * STAGE);
+  static constexpr int FIT = (227 * 1024 - int(sizeof(FewBars<WARPS>)) - JOIN) /
+                             (WARPS * (STAGE + SCALES));
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr size_t SMEM = size_t(FEW_WARPS) * STAGES * STAGE + JOIN + sizeof(FewBars);
+  static constexpr int RING = WARPS * STAGES * STAGE;
+  static constexpr size_t SMEM =
+      size_t(RING) + WARPS * STAGES * SCALES + JOIN + sizeof(FewBars<WARPS>);
   static_assert(STAGES >= 2, "the ring needs two stages");
 };
 
@@ -157,23 +162,25 @@ __device__ __forceinline__ uint32_t piece(int r, int ch) {
 }
 
 template <class T, class C, int HD, int NT>
-__global__ void __launch_bounds__(FEW_THREADS, 1)
+__global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
     attn_few_kernel(const __grid_constant__ FewArgs fa, Partials part) {
   using F = FewCfg<C, HD, NT>;
   constexpr bool E8 = F::E8;
   using M = typename std::conditional<E8, Fp16, T>::type;  // what the products multiply
-  constexpr int ROW = F::ROW, STAGES = F::STAGES, ROWS = F::ROWS;
+  constexpr int ROW = F::ROW, STAGES = F::STAGES, ROWS = F::ROWS, WARPS = F::WARPS;
+  constexpr int KEYS = F::KEYS;
   constexpr int STEPS = HD / 16;               // k-steps of a score, m-tiles of the output
   constexpr int PIECES = HD / (E8 ? 64 : 32);  // 16-byte pieces of a key row a lane reads
   const AttnArgs& a = fa.a;
   const int tq = fa.tq;
   extern __shared__ __align__(1024) unsigned char smem[];
-  FewBars& f = *reinterpret_cast<FewBars*>(smem + FEW_WARPS * STAGES * F::STAGE + F::JOIN);
+  unsigned char* join = smem + F::RING + WARPS * STAGES * F::SCALES;
+  FewBars<WARPS>& f = *reinterpret_cast<FewBars<WARPS>*>(join + F::JOIN);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Line<FEW_KEYS> line{a, tq, fa.extra};
+  const Line<KEYS> line{a, tq, fa.extra};
   if (warp == 0) {
     long long per;
-    const Cursor<FEW_KEYS> c = find_share<FEW_KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
+    const Cursor<KEYS> c = find_share<KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
     if (lane == 0) {
       f.per = int(per);
       f.start = c;
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       part.left[blockIdx.x] = none;
     }
   } else if (warp == 1 && lane == 0) {
-    for (int i = 0; i < FEW_WARPS * 8; ++i) mbar_init(&f.full[0][0] + i, 1);
+    for (int i = 0; i < WARPS * 8; ++i) mbar_init(&f.full[0][0] + i, 1);
     fence_barrier_init();
   } else if (warp == 2 && lane == 0) {
     prefetch_map(&fa.k);
@@ -190,11 +197,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   }
   __syncthreads();
   griddep_launch_dependents();
-  Cursor<FEW_KEYS> at = f.start, ahead = at;  // where the math is, where the copies are
+  Cursor<KEYS> at = f.start, ahead = at;  // where the math is, where the copies are
   if (at.left <= 0) return;
   const int per = f.per;
   const uint32_t ring = smem_addr(smem) + warp * (STAGES * F::STAGE);
-  unsigned char* join = smem + FEW_WARPS * STAGES * F::STAGE;
+  const uint32_t scales = smem_addr(smem) + F::RING + warp * (STAGES * F::SCALES);
   float* join_o = reinterpret_cast<float*>(join);  // [slot][ROWS][HD + 4]
   float2* join_ml = reinterpret_cast<float2*>(join + F::SLOTS * ROWS * (HD + 4) * 4);
 
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   // arrives as zeros, for one outside the cache.
   auto page_at = [&] {
     int page = a.c.n_pages;
-    const int key = ahead.j * FEW_KEYS + warp * 16;
+    const int key = ahead.j * KEYS + warp * 16;
     if (ahead.left > 0 && key < line.limit(ahead.s, ahead.i))
       page = a.table[(long long)ahead.b * a.table_stride + (key >> a.c.page_shift)];
     return page;
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   // copies of this warp's 16 keys of the tile at `ahead` into stage st
   auto fetch = [&](int st) {
     if (ahead.left <= 0) return;
-    const int key = ahead.j * FEW_KEYS + warp * 16;
+    const int key = ahead.j * KEYS + warp * 16;
     if (key < line.limit(ahead.s, ahead.i)) {
       const bool known = page >= 0 && page < a.c.n_pages;
       strange = (strange & ~(1u << st)) | (known ? 0u : 1u << st);
@@ -226,8 +233,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (E8 && known) {
           const long long sc =
               (((long long)page * a.c.kv_heads + ahead.h) << a.c.page_shift) + off;
-          bulk_load(dst + 32 * ROW, a.c.k_scale + sc, 64, bar);
-          bulk_load(dst + 32 * ROW + 64, a.c.v_scale + sc, 64, bar);
+          bulk_load(scales + st * 128, a.c.k_scale + sc, 64, bar);
+          bulk_load(scales + st * 128 + 64, a.c.v_scale + sc, 64, bar);
         }
       }
       __syncwarp();
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   int stage = 0;
   while (at.left > 0) {
     // ---- one segment: the tiles of one unit that lie in this share
-    const Cursor<FEW_KEYS> u = at;
+    const Cursor<KEYS> u = at;
     const int seg = u.segment(line);
     // queries: row r is token r / group of the tile, head r % group
     uint32_t q[NT][STEPS][2];
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       __syncwarp();
       // the stage of the step before this one, which every lane has left
       fetch(stage == 0 ? STAGES - 1 : stage - 1);
-      const int key = (u.j + step) * FEW_KEYS + warp * 16;
+      const int key = (u.j + step) * KEYS + warp * 16;
       if (key < line.limit(u.s, u.i)) {
         landed(stage);
         if (key + 16 > u.s.len) {
@@ -378,8 +385,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if constexpr (E8) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            kc[y] = __uint_as_float(lds32(vs + 16 * ROW + (g + 8 * y) * 4));
-            float sv = __uint_as_float(lds32(vs + 16 * ROW + 64 + (g + 8 * y) * 4));
+            kc[y] = __uint_as_float(lds32(scales + stage * 128 + (g + 8 * y) * 4));
+            float sv = __uint_as_float(lds32(scales + stage * 128 + 64 + (g + 8 * y) * 4));
             if (strange >> stage & 1) kc[y] = sv = 1.f;  // zeros, whose scales were not read
             sv = sv > 0.f ? sv : 1.f;                    // behind the sequence: masked
             vl[y] = lg2(sv);
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       at.skip(line, 1);
     }
 
-    // ---- join the warps, half of them at a time, and write the segment
+    // ---- join the warps, some of them at a time, and write the segment
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -499,38 +506,44 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           }
         }
     };
-    if (warp >= F::SLOTS) leave(warp - F::SLOTS);
-    __syncthreads();
-    if (warp < F::SLOTS) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int held = WARPS; held > F::SLOTS;) {  // warps that still hold something
+      const int n = held / 2 < F::SLOTS ? held / 2 : F::SLOTS;
+      if (warp >= held - n && warp < held) leave(warp - (held - n));
+      __syncthreads();
+      const int mine = warp - (held - 2 * n);
+      if (mine >= 0 && mine < n) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = nt * 8 + 2 * t + x;
-          const float2 ml = join_ml[warp * ROWS + r];
-          const float top = fmaxf(m[nt][x], ml.x), base = top == -INFINITY ? 0.f : top;
-          const float f0 = ex2(m[nt][x] - base), f1 = ex2(ml.x - base);
-          const float* from = join_o + (warp * ROWS + r) * (HD + 4);
-          l[nt][x] = l[nt][x] * f0 + ml.y * f1;
-          m[nt][x] = top;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < STEPS; ++i) {
-            float2 y;
-            if constexpr (E8)
-              y = *reinterpret_cast<const float2*>(from + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
-            else
-              y = make_float2(from[16 * i + g], from[16 * i + 8 + g]);
-            o[nt][i][x] = o[nt][i][x] * f0 + y.x * f1;
-            o[nt][i][2 + x] = o[nt][i][2 + x] * f0 + y.y * f1;
+          for (int x = 0; x < 2; ++x) {
+            const int r = nt * 8 + 2 * t + x;
+            const float2 ml = join_ml[mine * ROWS + r];
+            const float top = fmaxf(m[nt][x], ml.x), base = top == -INFINITY ? 0.f : top;
+            const float f0 = ex2(m[nt][x] - base), f1 = ex2(ml.x - base);
+            const float* from = join_o + (mine * ROWS + r) * (HD + 4);
+            l[nt][x] = l[nt][x] * f0 + ml.y * f1;
+            m[nt][x] = top;
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+              float2 y;
+              if constexpr (E8)
+                y = *reinterpret_cast<const float2*>(from + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
+              else
+                y = make_float2(from[16 * i + g], from[16 * i + 8 + g]);
+              o[nt][i][x] = o[nt][i][x] * f0 + y.x * f1;
+              o[nt][i][2 + x] = o[nt][i][2 + x] * f0 + y.y * f1;
+            }
           }
-        }
-      __syncwarp();
-      leave(warp);
+      }
+      held -= n;
+      __syncthreads();
     }
+    if (warp < F::SLOTS) leave(warp);
     __syncthreads();
     const bool whole = u.j == 0 && seg == u.n;
     const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
-    for (int x = threadIdx.x; x < ROWS * (HD / 4); x += FEW_THREADS) {
+    for (int x = threadIdx.x; x < ROWS * (HD / 4); x += F::THREADS) {
       const int r = x / (HD / 4), d = x % (HD / 4) * 4, token = u.i * tq + r / a.group;
       if (r >= tq * a.group || token >= u.s.n_new) continue;
       float top = -INFINITY;
