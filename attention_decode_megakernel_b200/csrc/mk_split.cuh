@@ -247,36 +247,53 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
   if (r >= tq * a.group || token >= s.n_new) return;
   constexpr int N = HD / 32;  // values of a lane, in pieces of 4 (2 for HD 64)
   constexpr int V = N < 4 ? N : 4;
-  float m = -INFINITY;
-  for (int k = lane; k <= u.more; k += 32) {
-    const size_t slot = k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
-    m = fmaxf(m, p.ml[slot * rows + r].x);
-  }
-  m = warp_max(m);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[N];
+  float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) o[i] = 0.f;
-#pragma unroll 8
-  for (int k = 0; k <= u.more; ++k) {
-    const size_t slot = k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
-    const float2 ml = p.ml[slot * rows + r];
-    const float f = exp2f(ml.x - base);
-    l += f * ml.y;
-    const float* src = p.o + (slot * rows + r) * HD + lane * V;
+  constexpr int BATCH = N == 8 ? 4 : 8;
+  for (int k0 = 0; k0 <= u.more; k0 += BATCH) {  // so many partials on their way at once
+    float2 ml[BATCH];
+    float x[BATCH][N];
 #pragma unroll
-    for (int i = 0; i < N; i += V) {
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src + i * 32);
-        o[i] += f * x.x;
-        o[i + 1] += f * x.y;
-        o[i + 2] += f * x.z;
-        o[i + 3] += f * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        o[0] += f * x.x;
-        o[1] += f * x.y;
+    for (int k = 0; k < BATCH; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[k][i] = 0.f;
+      if (k0 + k <= u.more) {
+        const size_t slot = k0 + k == 0 ? 2 * size_t(blockIdx.x) + 1
+                                        : 2 * (size_t(blockIdx.x) + k0 + k);
+        ml[k] = p.ml[slot * rows + r];
+        const float* src = p.o + (slot * rows + r) * HD + lane * V;
+#pragma unroll
+        for (int i = 0; i < N; i += V) {
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src + i * 32);
+            x[k][i] = y.x;
+            x[k][i + 1] = y.y;
+            x[k][i + 2] = y.z;
+            x[k][i + 3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            x[k][0] = y.x;
+            x[k][1] = y.y;
+          }
+        }
       }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+    const float base = top == -INFINITY ? 0.f : top, f0 = exp2f(m - base);
+    m = top;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] *= f0;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float f = exp2f(ml[k].x - base);
+      l += f * ml[k].y;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] += f * x[k][i];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -312,26 +329,45 @@ __global__ void __launch_bounds__(128)
   auto slot_of = [&](int k) {
     return k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
   };
-  float m = -INFINITY;
-  for (int k = 0; k <= u.more; ++k) m = fmaxf(m, p.ml[slot_of(k) * rows + r].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[16];
+  float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 2
-  for (int k = 0; k <= u.more; ++k) {
-    const size_t slot = slot_of(k);
-    const float2 ml = p.ml[slot * rows + r];
-    const float f = exp2f(ml.x - base);
-    l += f * ml.y;
-    const float4* src = reinterpret_cast<const float4*>(p.o) + (slot * (HD / 4) + d / 4) * rows + r;
+  for (int k0 = 0; k0 <= u.more; k0 += 4) {  // four partials on their way at once
+    float2 ml[4];
+    float4 x[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 x = src[i * rows];
-      o[4 * i] += f * x.x;
-      o[4 * i + 1] += f * x.y;
-      o[4 * i + 2] += f * x.z;
-      o[4 * i + 3] += f * x.w;
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k <= u.more) {
+        const size_t slot = slot_of(k0 + k);
+        ml[k] = p.ml[slot * rows + r];
+        const float4* src =
+            reinterpret_cast<const float4*>(p.o) + (slot * (HD / 4) + d / 4) * rows + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k][i] = src[i * rows];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+    const float base = top == -INFINITY ? 0.f : top, f0 = exp2f(m - base);
+    m = top;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= f0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = exp2f(ml[k].x - base);
+      l += f * ml[k].y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[4 * i] += f * x[k][i].x;
+        o[4 * i + 1] += f * x[k][i].y;
+        o[4 * i + 2] += f * x[k][i].z;
+        o[4 * i + 3] += f * x[k][i].w;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
