@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
-import struct
 from typing import Dict, Optional
 
 import numpy as np
@@ -381,9 +380,10 @@ def gemv_w4(codes, scales, x, y, stream=None):
 # call runs on torch's current stream of the tensors' device.
 #
 # A decoded token's calls take a few microseconds on the device, less than
-# ctypes needs for twenty arguments one by one.  So these five go through
-# libmk.so's mkw_ entries, which take the C ABI's arguments in its order as one
-# block of 64-bit words (floats as doubles) and call the entry of include/mk.h.
+# Python needs to look at seven tensors.  So a call first goes, as it is, to
+# libmk.so's mkp_ entry (csrc/mk_binding.cu), which looks at the tensors through
+# DLPack's C interface and refuses whatever does not fit exactly; what it
+# refuses is checked here, where the error says what is wrong.
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 _torch = None
@@ -438,33 +438,70 @@ def _head_rows(t, what):
 
 
 class _Call:
-    """One mkw_ entry: packs its arguments and runs it with `device` current."""
+    """One entry of the C ABI: quick(...) hands the objects over and is True when
+    the call was made; slow(...) makes it with plain numbers."""
 
-    def __init__(self, name, words):
-        self.name, self.pack, self.fn = name, struct.Struct(words + "q").pack, None
+    def __init__(self, name, quick_args):
+        self.name, self.quick_args, self.fn = name, quick_args, None
 
-    def __call__(self, device, stream, *args):
-        if self.fn is None:
-            fn = getattr(lib(), self.name.replace("mk_", "mkw_"))
-            fn.restype, fn.argtypes = C.c_int, [C.c_char_p]
+    def _load(self):
+        self.fn = _no_quick_way
+        L = _quick_lib()
+        if L is not None:
+            fn = getattr(L, self.name.replace("mk_", "mkp_"))
+            kinds = {"p": C.c_void_p, "i": C.c_int, "o": C.py_object, "d": C.c_double}
+            fn.restype, fn.argtypes = C.c_int, [kinds[k] for k in self.quick_args]
             self.fn = fn
-        if stream is None:
-            stream = _torch._C._cuda_getCurrentRawStream(device)
-        block = self.pack(*args, stream)
-        if device == _torch._C._cuda_getDevice():
-            rc = self.fn(block)
-        else:
-            with _torch.cuda.device(device):
-                rc = self.fn(block)
-        if rc != MK_OK:
+
+    def quick(self, *args):
+        if self.fn is None:
+            self._load()
+        try:
+            rc = self.fn(*args)
+        except Exception:  # an object that is no tensor, or one that DLPack cannot describe
+            return False
+        if rc > MK_OK:
             raise MkError(rc, self.name)
+        return rc == MK_OK
+
+    def slow(self, device, stream, *args):
+        if stream is None:
+            stream = _torch.cuda.current_stream(device).cuda_stream
+        with _torch.cuda.device(device):
+            _check(getattr(lib(), self.name)(*args, stream), self.name)
 
 
-_norm_rope_call = _Call("mk_qk_norm_rope", "20qdq")
-_kv_write_call = _Call("mk_kv_write", "10q")
-_kv_read_call = _Call("mk_kv_read", "10q")
-_paged_call = _Call("mk_attn_paged", "15qd3q")
-_packed_call = _Call("mk_attn_packed", "19qd3q")
+def _no_quick_way(*args):
+    return -1
+
+
+_quick = None
+
+
+def _quick_lib():
+    """libmk.so called with the interpreter lock held, or None without DLPack's C
+    interface (a tensor class of an older torch)."""
+    global _quick
+    if _quick is None:
+        _torch_types()
+        _quick = False
+        capsule = getattr(_torch.Tensor, "__dlpack_c_exchange_api__", None)
+        if capsule is not None:
+            get = C.pythonapi.PyCapsule_GetPointer
+            get.restype, get.argtypes = C.c_void_p, [C.py_object, C.c_char_p]
+            lib()
+            L = C.PyDLL(LIB_PATH)
+            L.mkp_init.restype, L.mkp_init.argtypes = C.c_int, [C.c_void_p, C.py_object]
+            if L.mkp_init(get(capsule, b"dlpack_exchange_api"), None) == 0:
+                _quick = L
+    return _quick or None
+
+
+_norm_rope_call = _Call("mk_qk_norm_rope", "poooooood")
+_kv_write_call = _Call("mk_kv_write", "piooo")
+_kv_read_call = _Call("mk_kv_read", "piooo")
+_paged_call = _Call("mk_attn_paged", "pioooooodo")
+_packed_call = _Call("mk_attn_packed", "oooooodo")
 
 
 class Rope:
@@ -489,6 +526,9 @@ def qk_norm_rope(rope, q, k, positions, q_out=None, k_out=None, q_gain=None, k_g
     """RMSNorm (where a gain [head_dim] is given) and rotation of every head of
     q [tokens][q_heads][head_dim] and k [tokens][kv_heads][head_dim] (or None),
     by positions int32 [tokens]; in place where no output is given."""
+    if stream is None and _norm_rope_call.quick(rope.address, q, k, positions, q_out, k_out, q_gain,
+                                                k_gain, eps):
+        return
     shape, dtype, code, dev = _head_rows(q, "q")
     tokens, heads, hd = shape
     qp, qts, qhs = _rows(q, "q", shape, dtype, dev)
@@ -505,7 +545,7 @@ def qk_norm_rope(rope, q, k, positions, q_out=None, k_out=None, q_gain=None, k_g
     qg = 0 if q_gain is None else _vector(q_gain, "q_gain", dtype, (hd,), dev)
     kg = 0 if k_gain is None else _vector(k_gain, "k_gain", dtype, (hd,), dev)
     pos = _vector(positions, "positions", _torch.int32, (tokens,), dev)
-    _norm_rope_call(dev, stream, rope.address, qp, qts, qhs, kp, kts, khs, qg, kg, pos, op, ots,
+    _norm_rope_call.slow(dev, stream, rope.address, qp, qts, qhs, kp, kts, khs, qg, kg, pos, op, ots,
                     ohs, okp, okts, okhs, tokens, heads, kv_heads, hd, eps, code)
 
 
@@ -552,15 +592,19 @@ def kv_write(cache, k, v, slots, stream=None):
     """Rows k, v [tokens][kv_heads][head_dim] (bfloat16, float16 or float32) into
     the cache: token t to slot slots[t] = page * page_size + position (int64);
     a slot outside the cache (-1) skips its token."""
+    if stream is None and _kv_write_call.quick(cache.address, cache.device, k, v, slots):
+        return
     dev, rows, sp, tokens, code = _move_args(cache, k, v, slots)
-    _kv_write_call(dev, stream, cache.address, *rows, sp, tokens, code)
+    _kv_write_call.slow(dev, stream, cache.address, *rows, sp, tokens, code)
 
 
 def kv_read(cache, slots, k_out, v_out, stream=None):
     """The rows of `slots` as values into k_out, v_out [tokens][kv_heads][head_dim];
     rows of slots outside the cache stay as they were."""
+    if stream is None and _kv_read_call.quick(cache.address, cache.device, slots, k_out, v_out):
+        return
     dev, rows, sp, tokens, code = _move_args(cache, k_out, v_out, slots)
-    _kv_read_call(dev, stream, cache.address, sp, tokens, *rows, code)
+    _kv_read_call.slow(dev, stream, cache.address, sp, tokens, *rows, code)
 
 
 def attn_workspace(head_dim, device="cuda"):
@@ -592,6 +636,11 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     which lie in the pages block_table[b] (int32).  out as q; lse float32
     [rows][q_heads] or None; scale head_dim ** -0.5 by default.  Rows behind
     cu_q[-1] stay as they were."""
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    if stream is None and workspace is not None and _paged_call.quick(
+            cache.address, cache.device, q, block_table, seq_lens, cu_q, out, lse, scale, workspace):
+        return
     shape, dtype, code, dev = _head_rows(q, "q")
     rows, heads, hd = shape
     if hd != cache.head_dim or dev != cache.device:
@@ -605,14 +654,19 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     sp = _vector(seq_lens, "seq_lens", i32, (batch,), dev)
     cp = _vector(cu_q, "cu_q", i32, (batch + 1,), dev)
     op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
-    _paged_call(dev, stream, cache.address, qp, qts, qhs, tp, pages, sp, cp, op, ots, ohs, lp,
-                rows, batch, heads, hd ** -0.5 if scale is None else scale, code, wp, wn)
+    _paged_call.slow(dev, stream, cache.address, qp, qts, qhs, tp, pages, sp, cp, op, ots, ohs, lp,
+                     rows, batch, heads, scale, code, wp, wn)
 
 
 def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, stream=None):
     """Causal attention of whole prompts packed one after another: rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [rows][q_heads][head_dim] and of k, v
     [rows][kv_heads][head_dim] are sequence b."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if stream is None and workspace is not None and _packed_call.quick(
+            q, k, v, cu_seqlens, out, lse, scale, workspace):
+        return
     shape, dtype, code, dev = _head_rows(q, "q")
     rows, heads, hd = shape
     kshape = k.shape
@@ -624,6 +678,5 @@ def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, 
     batch = cu_seqlens.shape[0] - 1
     cp = _vector(cu_seqlens, "cu_seqlens", _torch.int32, (batch + 1,), dev)
     op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
-    _packed_call(dev, stream, qp, qts, qhs, kp, kts, khs, vp, vts, vhs, cp, op, ots, ohs, lp,
-                 rows, batch, heads, kshape[1], hd, hd ** -0.5 if scale is None else scale, code,
-                 wp, wn)
+    _packed_call.slow(dev, stream, qp, qts, qhs, kp, kts, khs, vp, vts, vhs, cp, op, ots, ohs, lp,
+                      rows, batch, heads, kshape[1], hd, scale, code, wp, wn)

@@ -305,8 +305,3 @@ int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int
 }
 
 }  // extern "C"
-
-extern "C" {
-int mkw_attn_paged(const void* w) { return call(mk_attn_paged, w); }
-int mkw_attn_packed(const void* w) { return call(mk_attn_packed, w); }
-}  // extern "C"

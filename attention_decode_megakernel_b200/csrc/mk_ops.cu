@@ -185,9 +185,3 @@ int mk_kv_read(const mk_kv_cache* cache, const int64_t* slots, int tokens, void*
 }
 
 }  // extern "C"
-
-extern "C" {
-int mkw_qk_norm_rope(const void* w) { return call(mk_qk_norm_rope, w); }
-int mkw_kv_write(const void* w) { return call(mk_kv_write, w); }
-int mkw_kv_read(const void* w) { return call(mk_kv_read, w); }
-}  // extern "C"

@@ -1,13 +1,11 @@
 // mk_ops.cuh -- what the host sides of the operators share: status of a
-// launch, checks of rows and caches, choice of a kernel by type and head
-// dim, and the Python binding's calling form.
+// launch, checks of rows and caches, choice of a kernel by type and head dim.
 #pragma once
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <tuple>
 
 #include "mk.h"
 #include "mk_rows.cuh"
@@ -110,36 +108,4 @@ inline int blocks_for(long long items, int per_block, unsigned* blocks) {
   return MK_OK;
 }
 
-// ---- the Python binding's calling form -------------------------------------
-// The arguments of the entry of the same name, in its order, as 64-bit words
-// (floats as doubles): one conversion in place of twenty.
-struct Words {
-  const unsigned char* p;
-  int64_t word() {
-    int64_t w;
-    std::memcpy(&w, p, 8);
-    p += 8;
-    return w;
-  }
-  template <class T>
-  operator T*() {
-    return reinterpret_cast<T*>(word());
-  }
-  operator int64_t() { return word(); }
-  operator int() { return int(word()); }
-  operator size_t() { return size_t(word()); }
-  operator float() {
-    double d;
-    std::memcpy(&d, p, 8);
-    p += 8;
-    return float(d);
-  }
-};
-// Calls f with its parameters read one after another (braces keep the order).
-template <class... P>
-int call(int (*f)(P...), const void* block) {
-  Words w{static_cast<const unsigned char*>(block)};
-  const std::tuple<P...> a{static_cast<P>(w)...};
-  return std::apply(f, a);
-}
 }  // namespace
