@@ -58,29 +58,18 @@ int device_sms(int* dev, int* sms) {
   return MK_OK;
 }
 
-// The join of partial results, launched so that its CTAs are in place when the
-// kernel before it ends.
-int launch_join(void (*kernel)(mk::at::AttnArgs, mk::at::Partials, int, int), dim3 grid,
-                const mk::at::AttnArgs& a, const mk::at::Partials& p, int rows, int tq,
-                cudaStream_t st) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(128);
-  c.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  cudaLaunchKernelEx(&c, kernel, a, p, rows, tq);
-  return launched();
-}
-
 // What a unit costs besides its key tiles, in key tiles (mk_split.cuh), by sweeps: two
 // for tiles of rows (8 prompts of up to 4096 tokens at head_dim 128: 385 us at 0, 366 at 1,
 // 364 at 2, 377 at 4), two for few rows (64 sequences of up to 4096 over an e4m3 cache:
 // 51.3 us at 0, 50.2 at 1, 49.2 at 2 and more).
 constexpr int kFewExtra = 2, kFlashExtra = 2;
+
+// Calls whose sequences hold at most so many keys do not divide units over CTAs, and
+// have no join. Measured whole / divided (head_dim 256, 8 + 2 heads): one prompt of 520
+// tokens 13.9 / 15.4 us, of 780 17.3 / 17.0; 5 tokens over 128 keys 8.6 / 11.9, over 260
+// 11.8 / 12.3, over 520 15.5 / 12.2; one token over 64 keys 5.6 / 6.5, over 128 6.6 / 6.9,
+// over 260 9.4 / 7.4.
+constexpr int kWholePrompt = 640, kWholeChunk = 256, kWholeFew = 128;
 
 // cuTensorMapEncodeTiled through the runtime (no link against the driver library).
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -142,7 +131,7 @@ bool encode_rows(CUtensorMap* m, const void* base, const mk::PagedView& c, int r
 }
 
 template <class T, class C, int HD, int NT>
-int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+int launch_few(const mk::at::AttnArgs& a, long long longest, void* ws, int dev, int sms, cudaStream_t st) {
   using F = mk::at::FewCfg<C, HD, NT>;
   auto* kernel = &mk::at::attn_few_kernel<T, C, HD, NT>;
   static bool done[kMaxDevices] = {};
@@ -163,16 +152,17 @@ int launch_few(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream
   fa.tq = tq;
   fa.extra = kFewExtra;
   fa.least = 1;
+  fa.whole = longest <= kWholeFew;
   if (!encode_rows(&fa.k, a.c.k, a.c, F::ROW) || !encode_rows(&fa.v, a.c.v, a.c, F::ROW))
     return MK_ERR_UNSUPPORTED;
-  kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
-  const int rc = launched();
+  const int rc = launch(kernel, dim3(ctas), F::THREADS, F::SMEM, st, fa, p);
   const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
-  return rc != MK_OK ? rc : launch_join(mk::at::join_kernel<T, HD>, join, a, p, F::ROWS, tq, st);
+  if (rc != MK_OK || fa.whole) return rc;
+  return launch(mk::at::join_kernel<T, HD>, join, 128, 0, st, a, p, int(F::ROWS));
 }
 
 template <class T, class C, int HD, bool PAGED>
-int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStream_t st) {
+int launch_flash(const mk::at::AttnArgs& a, long long longest, void* ws, int dev, int sms, cudaStream_t st) {
   using F = mk::at::FlashCfg<C, HD>;
   auto* kernel = &mk::at::flash_kernel<T, C, HD, PAGED>;
   static bool done[kMaxDevices] = {};
@@ -190,6 +180,7 @@ int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStre
   fa.tq1 = 128 / a.group;
   fa.extra = kFlashExtra;
   fa.least = 1;
+  fa.whole = longest <= (PAGED ? kWholeChunk : kWholePrompt);
   fa.box_shift = 7;
   if (!encode_map(&fa.q, a.q, BF, HD, a.group, a.rows, a.kv_heads, a.q_hs, a.q_ts,
                   a.group * a.q_hs, a.group, fa.tq1))
@@ -216,11 +207,11 @@ int launch_flash(const mk::at::AttnArgs& a, void* ws, int dev, int sms, cudaStre
   constexpr int ROWS = F::NQ * 128;
   while (mk::at::partial_bytes(ctas, ROWS, HD) > mk_attn_ws_bytes(HD)) --ctas;
   const mk::at::Partials p = mk::at::carve(ws, ctas, ROWS, HD);
-  kernel<<<ctas, F::THREADS, F::SMEM, st>>>(fa, p);
-  const int rc = launched();
+  const int rc = launch(kernel, dim3(ctas), F::THREADS, F::SMEM, st, fa, p);
   const int tq = F::NQ * fa.tq1;
   const dim3 join(ctas, (tq * a.group + 31) / 32 * (HD / 64));
-  return rc != MK_OK ? rc : launch_join(mk::at::join_tiles_kernel<T, HD>, join, a, p, ROWS, tq, st);
+  if (rc != MK_OK || fa.whole) return rc;
+  return launch(mk::at::join_tiles_kernel<T, HD>, join, 128, 0, st, a, p, int(ROWS));
 }
 
 }  // namespace
@@ -255,6 +246,7 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   rc = device_sms(&dev, &sms);
   if (rc != MK_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long longest = (long long)table_stride * cache->page_size;
   const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
   by_half_type(dtype, [&](auto t) {
     by_head_dim(cache->head_dim, [&](auto d) {
@@ -262,14 +254,14 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
       constexpr int HD = decltype(d)::value;
       const bool e8 = cache->dtype == MK_E4M3;
       if (unit <= 8)
-        rc = e8 ? launch_few<T, mk::E4m3, HD, 1>(a, workspace, dev, sms, st)
-                : launch_few<T, T, HD, 1>(a, workspace, dev, sms, st);
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 1>(a, longest, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 1>(a, longest, workspace, dev, sms, st);
       else if (unit <= 16)
-        rc = e8 ? launch_few<T, mk::E4m3, HD, 2>(a, workspace, dev, sms, st)
-                : launch_few<T, T, HD, 2>(a, workspace, dev, sms, st);
+        rc = e8 ? launch_few<T, mk::E4m3, HD, 2>(a, longest, workspace, dev, sms, st)
+                : launch_few<T, T, HD, 2>(a, longest, workspace, dev, sms, st);
       else
-        rc = e8 ? launch_flash<T, mk::E4m3, HD, true>(a, workspace, dev, sms, st)
-                : launch_flash<T, T, HD, true>(a, workspace, dev, sms, st);
+        rc = e8 ? launch_flash<T, mk::E4m3, HD, true>(a, longest, workspace, dev, sms, st)
+                : launch_flash<T, T, HD, true>(a, longest, workspace, dev, sms, st);
     });
   });
   return rc;
@@ -294,11 +286,12 @@ int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int
   int dev, sms;
   rc = device_sms(&dev, &sms);
   if (rc != MK_OK) return rc;
+  const long long longest = rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_half_type(dtype, [&](auto t) {
     by_head_dim(head_dim, [&](auto d) {
       using T = typename decltype(t)::type;
-      rc = launch_flash<T, T, decltype(d)::value, false>(a, workspace, dev, sms, st);
+      rc = launch_flash<T, T, decltype(d)::value, false>(a, longest, workspace, dev, sms, st);
     });
   });
   return rc;

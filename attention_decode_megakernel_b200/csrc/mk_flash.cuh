@@ -114,7 +114,7 @@ struct FlashArgs {
   CUtensorMap q, k, v;  // q: (dim, head of the group, row, key head); k, v: (dim, position, head, page)
   int tq1;              // tokens of a row tile
   int box_shift;        // log2 of the positions of a K box
-  int extra, least;     // of the line (mk_split.cuh)
+  int extra, least, whole;  // of the line (mk_split.cuh)
 };
 
 // Called by whole warps; the answer is the same in every lane.
@@ -208,10 +208,12 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   FlashBars<NQ>& f =
       *reinterpret_cast<FlashBars<NQ>*>(q_size + (E8 ? 4 * NQ * 128 : 0));
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  const Line<KEYS> line{a, NQ * fa.tq1, fa.extra};
+  const Line<KEYS> line{a, NQ * fa.tq1, fa.extra, fa.whole != 0};
   const int tq1 = fa.tq1, tile_rows = tq1 * a.group;
 
+  griddep_launch_dependents();
   if (warp == 0) {
+    griddep_wait();
     long long per;
     const Cursor<KEYS> c = find_share<KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
     if (lane == 0) {
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
+  griddep_wait();
   const uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
   Cursor<KEYS> at = f.start;
   make_uniform(at);
@@ -761,7 +763,9 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         }
       }
       if (s == 0 && half == 0 && r == 0 && u.j == 0 && !whole) {
-        Left left = {u.b, u.h, u.i, (u.n - seg + f.per - 1) / f.per};
+        const int tokens = u.s.n_new - u.i * NQ * tq1;
+        Left left = {(u.n - seg + f.per - 1) / f.per, u.s.first + u.i * NQ * tq1, u.h,
+                     (tokens < NQ * tq1 ? tokens : NQ * tq1) * a.group};
         part.left[blockIdx.x] = left;
       }
       tc_fence_before();

@@ -153,6 +153,8 @@ template <class T, class C, int HD>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant__ MoveArgs a) {
   using R = RowType<T>;
   constexpr int VEC = R::VEC, LANES = HD / (2 * VEC);
+  griddep_launch_dependents();
+  griddep_wait();
   const int s = threadIdx.x % LANES, head = blockIdx.y;
   const unsigned token = blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
   const bool live = token < unsigned(a.tokens);  // the others still take part in shuffles
@@ -197,6 +199,8 @@ template <class T, class C, int HD>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(const __grid_constant__ MoveArgs a) {
   using R = RowType<T>;
   constexpr int VEC = R::VEC, LANES = HD / (2 * VEC);
+  griddep_launch_dependents();
+  griddep_wait();
   const int s = threadIdx.x % LANES, head = blockIdx.y;
   const unsigned token = blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
   if (token >= unsigned(a.tokens)) return;

@@ -131,6 +131,8 @@ int mk_qk_norm_rope(const mk_rope* rope, const void* q, int64_t q_ts, int64_t q_
   if (parts > 65535) return MK_ERR_UNSUPPORTED;
   const dim3 grid(blocks, parts);
   const size_t smem = size_t(groups) * rope->rot_dim * 4;
+  // (Launched to start while the kernel before it ends, as the other operators are, 520
+  // tokens took 7.7 us one after another in a graph, not 5.1.)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_row_type(dtype, [&](auto t) {
     by_head_dim(head_dim, [&](auto d) {
@@ -150,17 +152,17 @@ int mk_kv_write(const mk_kv_cache* cache, const void* k, int64_t k_ts, int64_t k
   if (rc != MK_OK || tokens == 0) return rc;
   a.k = static_cast<const unsigned char*>(k);
   a.v = static_cast<const unsigned char*>(v);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int status = MK_OK;
   by_row_type(dtype, [&](auto t) {
     by_cache_type(cache->dtype, [&](auto c) {
       by_head_dim(cache->head_dim, [&](auto d) {
-        mk::kv::kv_write_kernel<typename decltype(t)::type, typename decltype(c)::type,
-                                decltype(d)::value>
-            <<<dim3(blocks, cache->kv_heads), mk::kv::THREADS, 0, st>>>(a);
+        status = launch(mk::kv::kv_write_kernel<typename decltype(t)::type,
+                                             typename decltype(c)::type, decltype(d)::value>,
+                        dim3(blocks, cache->kv_heads), mk::kv::THREADS, 0, stream, a);
       });
     });
   });
-  return launched();
+  return status;
 }
 
 int mk_kv_read(const mk_kv_cache* cache, const int64_t* slots, int tokens, void* k, int64_t k_ts,
@@ -171,17 +173,17 @@ int mk_kv_read(const mk_kv_cache* cache, const int64_t* slots, int tokens, void*
   if (rc != MK_OK || tokens == 0) return rc;
   a.k_out = static_cast<unsigned char*>(k);
   a.v_out = static_cast<unsigned char*>(v);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int status = MK_OK;
   by_row_type(dtype, [&](auto t) {
     by_cache_type(cache->dtype, [&](auto c) {
       by_head_dim(cache->head_dim, [&](auto d) {
-        mk::kv::kv_read_kernel<typename decltype(t)::type, typename decltype(c)::type,
-                               decltype(d)::value>
-            <<<dim3(blocks, cache->kv_heads), mk::kv::THREADS, 0, st>>>(a);
+        status = launch(mk::kv::kv_read_kernel<typename decltype(t)::type,
+                                             typename decltype(c)::type, decltype(d)::value>,
+                        dim3(blocks, cache->kv_heads), mk::kv::THREADS, 0, stream, a);
       });
     });
   });
-  return launched();
+  return status;
 }
 
 }  // extern "C"

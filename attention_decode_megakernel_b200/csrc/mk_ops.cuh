@@ -67,6 +67,25 @@ inline int cache_view(const mk_kv_cache* c, mk::PagedView* v) {
   return MK_OK;
 }
 
+// Launch `kernel` so that its CTAs may start while the kernel before it in the
+// stream ends, if that one allows it; it waits (griddep_wait) before it touches memory.
+template <class... P, class... A>
+int launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, void* stream,
+           const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, args...);
+  return launched();
+}
+
 template <class T>
 struct Tag {
   using type = T;

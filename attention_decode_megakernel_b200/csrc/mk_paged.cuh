@@ -76,7 +76,7 @@ struct FewCfg {
 struct FewArgs {
   AttnArgs a;
   CUtensorMap k, v;  // (dim within 128 bytes, position, column of 128 bytes, head, page)
-  int tq, extra, least;
+  int tq, extra, least, whole;
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c1, int c3,
@@ -177,8 +177,10 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
   unsigned char* join = smem + F::RING + WARPS * STAGES * F::SCALES;
   FewBars<WARPS>& f = *reinterpret_cast<FewBars<WARPS>*>(join + F::JOIN);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Line<KEYS> line{a, tq, fa.extra};
+  const Line<KEYS> line{a, tq, fa.extra, fa.whole != 0};
+  griddep_launch_dependents();
   if (warp == 0) {
+    griddep_wait();
     long long per;
     const Cursor<KEYS> c = find_share<KEYS>(line, blockIdx.x, gridDim.x, fa.least, per);
     if (lane == 0) {
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
     prefetch_map(&fa.v);
   }
   __syncthreads();
-  griddep_launch_dependents();
+  griddep_wait();
   Cursor<KEYS> at = f.start, ahead = at;  // where the math is, where the copies are
   if (at.left <= 0) return;
   const int per = f.per;
@@ -579,7 +581,9 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
       }
     }
     if (u.j == 0 && !whole && threadIdx.x == 0) {
-      Left left = {u.b, u.h, u.i, (u.n - seg + per - 1) / per};
+      const int tokens = u.s.n_new - u.i * tq;
+      Left left = {(u.n - seg + per - 1) / per, u.s.first + u.i * tq, u.h,
+                   (tokens < tq ? tokens : tq) * a.group};
       part.left[blockIdx.x] = left;
     }
     __syncthreads();  // the join buffer is free again

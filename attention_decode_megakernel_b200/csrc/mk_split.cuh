@@ -70,6 +70,7 @@ template <int KT>
 struct Line {
   const AttnArgs& a;
   int tq, extra;
+  bool whole;  // units are not divided: a CTA finishes those that begin in its share
 
   __device__ int row_tiles(const Seq& s) const { return (s.n_new + tq - 1) / tq; }
   // keys that the last token of row tile i sees (may be negative)
@@ -88,8 +89,13 @@ struct Line {
     const int none = past < 0 ? (-past) / tq : 0;
     if (none >= x) return x;
     const long long b = (long long)(none + 1) * tq + past + KT - 1, n = x - none;
-    if (b + n * tq < (1ll << 31))
-      return none + floor_sum<unsigned>(unsigned(n), KT, unsigned(tq), unsigned(b));
+    if (b + n * tq < (1ll << 31)) {
+      // the first step by the constant KT, a power of two; none or one follow as a rule
+      const unsigned a0 = unsigned(tq) % KT, b0 = unsigned(b) % KT, y = a0 * unsigned(n) + b0;
+      const long long s = (long long)(unsigned(tq) / KT) * (n * (n - 1) / 2) +
+                          (long long)(unsigned(b) / KT) * n;
+      return none + s + (y < KT ? 0 : floor_sum<unsigned>(y / KT, a0, KT, y % KT));
+    }
     return none + floor_sum<unsigned long long>(n, KT, tq, b);
   }
   // the length of the first x row tiles, and of one head of the sequence
@@ -113,15 +119,19 @@ struct Cursor {
   // tiles of the present unit that lie in this share
   __device__ int segment(const Line<KT>& line) const {
     const int end = at + left - line.extra;
-    return (end < n ? end : n) - j;
+    return (end < n && !line.whole ? end : n) - j;
   }
   // past `tiles` of them; at the unit's end, on to the next unit
   __device__ void skip(const Line<KT>& line, int tiles) {
     j += tiles;
     left -= line.extra + j - at;
     at = line.extra + j;
-    if (j < n || left <= line.extra) {
-      if (j == n) left = 0;  // the share ends before the next unit's first tile
+    if (j < n) {
+      if (line.whole && left < 1) left = 1;  // past the share's end, to the unit's
+      return;
+    }
+    if (left <= line.extra) {
+      left = 0;  // the share ends before the next unit's first tile
       return;
     }
     at = j = 0;
@@ -147,11 +157,15 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
                                                  int least, long long& per) {
   const AttnArgs& a = line.a;
   const int lane = threadIdx.x & 31;
-  long long total = 0, mine = 0;
+  long long total = 0, head = 0;  // length of a head of the lane's sequence
+  Seq s = {};
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    mine = b < a.batch ? line.all(seq_of(a, b)) * a.kv_heads : 0;
-    long long w = mine;
+    head = 0;
+    if (b0 + lane < a.batch) {
+      s = seq_of(a, b0 + lane);
+      head = line.all(s);
+    }
+    long long w = head * a.kv_heads;
     for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     total += w;
   }
@@ -161,11 +175,17 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
   const long long at = cta * per;
   if (at >= total) return c;
   c.left = int(total - at < per ? total - at : per);
-  // the sequence that holds tile `at`
+  // the sequence that holds place `at`
   long long before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    if (a.batch > 32) mine = b < a.batch ? line.all(seq_of(a, b)) * a.kv_heads : 0;
+    if (a.batch > 32) {
+      head = 0;
+      if (b0 + lane < a.batch) {
+        s = seq_of(a, b0 + lane);
+        head = line.all(s);
+      }
+    }
+    const long long mine = head * a.kv_heads;
     long long sum = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long up = __shfl_up_sync(0xffffffffu, sum, o);
@@ -175,30 +195,39 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
     if (past) {
       const int found = __ffs(past) - 1;
       before += __shfl_sync(0xffffffffu, sum - mine, found);
+      head = __shfl_sync(0xffffffffu, head, found);
       c.b = b0 + found;
+      c.s.first = __shfl_sync(0xffffffffu, s.first, found);
+      c.s.n_new = __shfl_sync(0xffffffffu, s.n_new, found);
+      c.s.len = __shfl_sync(0xffffffffu, s.len, found);
       break;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  c.s = seq_of(a, c.b);
   c.nq = line.row_tiles(c.s);
   long long off = at - before;
-  const long long head = line.all(c.s);
   c.h = int(off / head);
   off -= c.h * head;
   // the last row tile that starts at or before `off`: 32 places at a time
   int lo = 0, span = c.nq;  // it is one of lo .. lo + span - 1
+  long long start = 0;      // where it starts
   while (span > 1) {
     const int step = (span + 31) / 32, x = lo + lane * step;
-    const bool at_or_before = x == 0 || (lane * step < span && line.length(c.s, x) <= off);
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, at_or_before));
+    const long long here = lane * step < span ? line.length(c.s, x) : off + 1;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, here <= off));
+    start = __shfl_sync(0xffffffffu, here, last);
     span = span - last * step < step ? span - last * step : step;
     lo += last * step;
   }
   c.i = lo;
-  c.at = int(off - line.length(c.s, lo));
+  c.at = int(off - start);
   c.j = c.at > line.extra ? c.at - line.extra : 0;
   c.n = line.tiles(c.s, c.i);
+  if (line.whole && c.j > 0) {
+    // whole units only: the unit that the last CTA began is that one's
+    c.skip(line, c.n - c.j);
+    return c;
+  }
   if (c.at + c.left <= line.extra) c.left = 0;
   return c;
 }
@@ -207,8 +236,10 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
 // (few rows) or [HD / 4][R] float4 (tiles of rows), their {maximum, sum} [R], and
 // for each CTA the unit that it left unfinished.
 struct Left {
-  int b, h, i;
-  int more;  // CTAs behind this one that hold the rest; 0: nothing was left
+  int more;   // CTAs behind this one that hold the rest; 0: nothing was left
+  int first;  // the unit's first row
+  int h;
+  int rows;   // its rows: tokens times the group
 };
 struct Partials {
   float* o;
@@ -237,14 +268,14 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 constexpr int JOIN_ROWS = 4;
 template <class T, int HD>
 __global__ void __launch_bounds__(JOIN_ROWS * 32)
-    join_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows, int tq) {
+    join_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows) {
+  griddep_launch_dependents();
   griddep_wait();
   const Left u = p.left[blockIdx.x];
   if (u.more <= 0) return;
   const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const Seq s = seq_of(a, u.b);
-  const int first = s.first, token = u.i * tq + r / a.group;
-  if (r >= tq * a.group || token >= s.n_new) return;
+  if (r >= u.rows) return;
+  const long long row = u.first + r / a.group;
   constexpr int N = HD / 32;  // values of a lane, in pieces of 4 (2 for HD 64)
   constexpr int V = N < 4 ? N : 4;
   float m = -INFINITY, l = 0.f, o[N];
@@ -298,7 +329,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int head = u.h * a.group + r % a.group;
-  unsigned char* out = a.out + ((long long)(first + token) * a.o_ts + head * a.o_hs + lane * V) * 2;
+  unsigned char* out = a.out + (row * a.o_ts + head * a.o_hs + lane * V) * 2;
 #pragma unroll
   for (int i = 0; i < N; i += V) {
     if constexpr (V == 4) {
@@ -310,22 +341,22 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
       *reinterpret_cast<uint32_t*>(out) = RowType<T>::pack2(o[0] * inv, o[1] * inv);
     }
   }
-  if (a.lse && lane == 0) a.lse[(long long)(first + token) * a.q_heads + head] = row_lse(m, l);
+  if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = row_lse(m, l);
 }
 
 // The same for partials [HD / 4][rows]: block (c, y) takes 32 rows, a lane for each,
 // and 64 columns, 16 to a warp.
 template <class T, int HD>
 __global__ void __launch_bounds__(128)
-    join_tiles_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows, int tq) {
+    join_tiles_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows) {
+  griddep_launch_dependents();
   griddep_wait();
   const Left u = p.left[blockIdx.x];
   if (u.more <= 0) return;
-  const Seq s = seq_of(a, u.b);
   const int lane = threadIdx.x & 31, r = blockIdx.y / (HD / 64) * 32 + lane;
   const int d = blockIdx.y % (HD / 64) * 64 + (threadIdx.x >> 5) * 16;
-  const int token = u.i * tq + r / a.group;
-  if (r >= tq * a.group || token >= s.n_new) return;
+  if (r >= u.rows) return;
+  const long long row = u.first + r / a.group;
   auto slot_of = [&](int k) {
     return k == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * (size_t(blockIdx.x) + k);
   };
@@ -372,7 +403,6 @@ __global__ void __launch_bounds__(128)
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int head = u.h * a.group + r % a.group;
-  const long long row = s.first + token;
   uint4* out = reinterpret_cast<uint4*>(a.out + (row * a.o_ts + head * a.o_hs + d) * 2);
 #pragma unroll
   for (int i = 0; i < 16; i += 8)
