@@ -491,8 +491,9 @@ def _quick_lib():
             get.restype, get.argtypes = C.c_void_p, [C.py_object, C.c_char_p]
             lib()
             L = C.PyDLL(LIB_PATH)
-            L.mkp_init.restype, L.mkp_init.argtypes = C.c_int, [C.c_void_p, C.py_object]
-            if L.mkp_init(get(capsule, b"dlpack_exchange_api"), None) == 0:
+            L.mkp_init.restype = C.c_int
+            L.mkp_init.argtypes = [C.c_void_p, C.py_object, C.py_object]
+            if L.mkp_init(get(capsule, b"dlpack_exchange_api"), _torch.Tensor, None) == 0:
                 _quick = L
     return _quick or None
 

@@ -39,8 +39,15 @@ struct DlExchange {
 constexpr int MKP_SLOW = -1;
 constexpr int kCuda = 2, kInt = 0, kUint = 1, kFloat = 2, kBfloat = 4;
 
+// The head of every Python object.
+struct PyHead {
+  intptr_t references;
+  void* type;
+};
+
 const DlExchange* g_dl = nullptr;
 void* g_none = nullptr;
+void* g_tensor_type = nullptr;  // the exchange functions take objects of this class alone
 
 struct Slow {};  // thrown and caught in this file
 
@@ -57,7 +64,8 @@ struct Args {
 
   DlTensor view(void* object) {
     DlTensor t;
-    if (!g_dl || g_dl->view(object, &t) != 0 || t.device_type != kCuda || !t.strides) throw Slow{};
+    if (!g_dl || static_cast<PyHead*>(object)->type != g_tensor_type ||
+        g_dl->view(object, &t) != 0 || t.device_type != kCuda || !t.strides) throw Slow{};
     if (device < 0) {
       int now;
       if (cudaGetDevice(&now) != cudaSuccess || now != t.device) throw Slow{};
@@ -138,12 +146,14 @@ int quick(F f) {
 
 extern "C" {
 
-// The exchange table of the tensor class and the object that stands for nothing.
-int mkp_init(const void* exchange, void* none) {
+// The exchange table of the tensor class, that class, and the object that stands for
+// nothing.
+int mkp_init(const void* exchange, void* tensor_type, void* none) {
   const DlExchange* dl = static_cast<const DlExchange*>(exchange);
   if (!dl || dl->major != 1 || !dl->view || !dl->stream) return MKP_SLOW;
-  g_dl = dl;
+  g_tensor_type = tensor_type;
   g_none = none;
+  g_dl = dl;
   return 0;
 }
 

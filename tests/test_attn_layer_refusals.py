@@ -256,3 +256,15 @@ def test_reference_e4m3_against_torch():
     assert torch.equal(codes[:, 0].float(), x.to(torch.float8_e4m3fn).float())
     rows = torch.tensor([[448.0, 1.0], [449.0, 1.0], [0.0, 0.0], [1e-30, 0.0], [1.75, -1.0]])
     assert ref.to_e4m3(rows)[1].tolist() == [1.0, 2.0, 2.0 ** -64, 2.0 ** -64, 2.0 ** -8]
+
+
+def test_binding_takes_no_other_objects():
+    """What is no tensor (or a tensor of a subclass) is not handed to the quick way's
+    tensor functions; the long way answers for it."""
+    torch = pytest.importorskip("torch")
+    q, pos = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    rope = mk.Rope(64, 1e4)
+    for bad in ([1, 2], "text", 5, None, object(), torch.nn.Parameter(torch.zeros(3, 4, 64)), q):
+        assert not mk._norm_rope_call.quick(rope.address, bad, q, pos, None, None, None, None, 1e-6)
+        with pytest.raises((ValueError, AttributeError)):
+            mk.qk_norm_rope(rope, bad, None, pos)
