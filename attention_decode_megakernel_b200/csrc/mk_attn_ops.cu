@@ -156,9 +156,9 @@ int launch_few(const mk::at::AttnArgs& a, long long longest, void* ws, int dev, 
   if (!encode_rows(&fa.k, a.c.k, a.c, F::ROW) || !encode_rows(&fa.v, a.c.v, a.c, F::ROW))
     return MK_ERR_UNSUPPORTED;
   const int rc = launch(kernel, dim3(ctas), F::THREADS, F::SMEM, st, fa, p);
-  const dim3 join(ctas, (tq * a.group + mk::at::JOIN_ROWS - 1) / mk::at::JOIN_ROWS);
   if (rc != MK_OK || fa.whole) return rc;
-  return launch(mk::at::join_kernel<T, HD>, join, 128, 0, st, a, p, int(F::ROWS));
+  return launch(mk::at::join_kernel<T, HD>, dim3(ctas, tq * a.group),
+                mk::at::JOIN_SPLIT * 32, 0, st, a, p, int(F::ROWS));
 }
 
 template <class T, class C, int HD, bool PAGED>

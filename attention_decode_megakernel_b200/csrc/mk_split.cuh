@@ -262,27 +262,44 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : l == 0.f ? -INFINITY : l;
 }
 
-// Joins the partials of the unit that CTA blockIdx.x left unfinished: block
-// (c, y) takes the rows y * ROWS .. of it, a warp for each row; the lanes
-// hold the row's values, the partials are read in the CTAs' order.
-constexpr int JOIN_ROWS = 4;
+// Adds {m1, l1, o1} to {m, l, o}, both sums of weights 2^(x - m).
+template <int N>
+__device__ __forceinline__ void join_in(float& m, float& l, float (&o)[N], float m1, float l1,
+                                        const float* o1, int step) {
+  const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.f : top;
+  const float f0 = exp2f(m - base), f1 = exp2f(m1 - base);
+  m = top;
+  l = l * f0 + l1 * f1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = o[i] * f0 + o1[i * step] * f1;
+}
+
+// Joins the partials of the unit that CTA blockIdx.x left unfinished: block (c, r) takes
+// row r of it; the lanes of a warp hold the row's values.  JOIN_SPLIT warps share the
+// partials, a run of them each, read in the CTAs' order and several at once, and the first
+// adds up the runs in their order: one token over 32768 keys leaves 74 partials a head
+// (head_dim 256: 29.9 us with one warp, 21.6 with four, 21.0 with six, 20.5 with eight, which
+// cost 64 sequences 0.3 us).  A few partials are one warp's.
+constexpr int JOIN_SPLIT = 6;
 template <class T, int HD>
-__global__ void __launch_bounds__(JOIN_ROWS * 32)
+__global__ void __launch_bounds__(JOIN_SPLIT * 32)
     join_kernel(const __grid_constant__ AttnArgs a, Partials p, int rows) {
   griddep_launch_dependents();
   griddep_wait();
   const Left u = p.left[blockIdx.x];
-  if (u.more <= 0) return;
-  const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= u.rows) return;
-  const long long row = u.first + r / a.group;
+  const int r = blockIdx.y, lane = threadIdx.x & 31, split = threadIdx.x >> 5;
+  if (u.more <= 0 || r >= u.rows) return;
+  __shared__ float runs[JOIN_SPLIT - 1][HD / 32 + 2][32];
   constexpr int N = HD / 32;  // values of a lane, in pieces of 4 (2 for HD 64)
   constexpr int V = N < 4 ? N : 4;
   float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) o[i] = 0.f;
   constexpr int BATCH = N == 8 ? 4 : 8;
-  for (int k0 = 0; k0 <= u.more; k0 += BATCH) {  // so many partials on their way at once
+  const int n = u.more + 1, share = (n + JOIN_SPLIT - 1) / JOIN_SPLIT;
+  const int run = n <= 2 * BATCH ? n : share;  // partials of a warp
+  const int k1 = min(n, (split + 1) * run);
+  for (int k0 = split * run; k0 < k1; k0 += BATCH) {  // so many partials on their way at once
     float2 ml[BATCH];
     float x[BATCH][N];
 #pragma unroll
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
       ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) x[k][i] = 0.f;
-      if (k0 + k <= u.more) {
+      if (k0 + k < k1) {
         const size_t slot = k0 + k == 0 ? 2 * size_t(blockIdx.x) + 1
                                         : 2 * (size_t(blockIdx.x) + k0 + k);
         ml[k] = p.ml[slot * rows + r];
@@ -327,7 +344,22 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32)
       for (int i = 0; i < N; ++i) o[i] += f * x[k][i];
     }
   }
+  if (run < n) {
+    if (split > 0) {
+      float(*to)[32] = runs[split - 1];
+      to[N][lane] = m;
+      to[N + 1][lane] = l;
+#pragma unroll
+      for (int i = 0; i < N; ++i) to[i][lane] = o[i];
+    }
+    __syncthreads();
+    if (split == 0)
+      for (int s = 0; s < JOIN_SPLIT - 1; ++s)
+        join_in<N>(m, l, o, runs[s][N][lane], runs[s][N + 1][lane], &runs[s][0][lane], 32);
+  }
+  if (split > 0) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const long long row = u.first + r / a.group;
   const int head = u.h * a.group + r % a.group;
   unsigned char* out = a.out + (row * a.o_ts + head * a.o_hs + lane * V) * 2;
 #pragma unroll

@@ -133,6 +133,16 @@ def test_paged_long_context(mk, dtype, kind, t):
     run_paged(mk, gen, [t], [20011], 8, 2, 128, 64, dtype, kind)
 
 
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_paged_one_sequence_in_few_and_many_parts(mk, kind, hd):
+    """Partial results of 1 to 148 stretches of keys: one warp's and several warps' joins."""
+    gen = torch.Generator(device="cuda").manual_seed(hd + 1)
+    for n in (129, 513, 700, 1025, 1290, 2000, 4700, 9700):
+        run_paged(mk, gen, [1], [n], 2, 1, hd, 32, BF, kind)
+    run_paged(mk, gen, [3], [5000], 4, 1, hd, 32, BF, kind)
+
+
 def test_paged_peaked_scores(mk):
     """Scores of several hundred, the largest in any place: the running maximum."""
     gen = torch.Generator(device="cuda").manual_seed(13)
