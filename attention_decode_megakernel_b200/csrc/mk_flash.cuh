@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   const int tq1 = fa.tq1, tile_rows = tq1 * a.group;
 
   griddep_launch_dependents();
+  warm_l2(a);
   if (warp == 0) {
     griddep_wait();
     long long per;

@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const Line<KEYS> line{a, tq, fa.extra, fa.whole != 0};
   griddep_launch_dependents();
+  warm_l2(a);
   if (warp == 0) {
     griddep_wait();
     long long per;

@@ -149,6 +149,21 @@ struct Cursor {
   }
 };
 
+// Brings what find_share and the page lookups read into L2: before the wait for the
+// kernel in front, as a hint that takes no values.  Called by all threads of the call's
+// CTAs (300 sequences of 300 keys: 44.2 to 43.2 us, one of 32768: 20.9 to 20.5).
+__device__ __forceinline__ void warm_l2(const AttnArgs& a) {
+  auto touch = [](const int* from, long long n, long long line) {
+    if (line * 32 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + line * 32));
+  };
+  const long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  touch(a.cu_q, a.batch + 1, x);
+  if (a.table) {
+    touch(a.seq_lens, a.batch, x);
+    touch(a.table, a.batch * (long long)a.table_stride, x);
+  }
+}
+
 // The place and share of CTA `cta` of `ctas`, shares of at least `least`;
 // `per` receives a share's length.  Called by one whole warp with all
 // lanes; the result is the same in every lane.
