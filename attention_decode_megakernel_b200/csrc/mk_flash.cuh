@@ -11,8 +11,9 @@
 //                    TMEM, weights back as 16-bit pairs over the scores' columns
 //   O += P V    P from TMEM, V as it lies in memory (MN-major)
 //
-// Warps: one TMA producer, two MMA issuers, two softmax warpgroups.  While these work on one tile, the tensor cores run the other stream's
-// products (or the next tile's scores and the last one's output).  The maximum of a row is raised only when a score
+// Warps: one TMA producer, two MMA issuers, two softmax warpgroups.  While these work
+// on one tile, the tensor cores run the other stream's products (or the next tile's
+// scores and the last one's output).  The maximum of a row is raised only when a score
 // passes it by far (mk_paged.cuh, Weights), and only then is O rescaled in TMEM;
 // the sum of weights is kept in fp32 from the unrounded weights.
 //
@@ -275,261 +276,261 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
   // common point would be held to the smallest share.
   if (warp < 4) {
     fewer_registers<F::REGS_REST>();
-  if (warp == 0) {
-    // ---- TMA producer: queries, and keys and values unless they are converted
-    Ring<STAGES> to;
-    int seg_no = 0;
-    while (at.left > 0) {
-      const int seg = at.segment(line), ns = streams(at);
-      bool ok = seg_no == 0 || flash_wait(&f.q_empty, (seg_no - 1) & 1, &f.gave_up);
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
-        for (int s = 0; s < ns; ++s)
-          for (int c = 0; c < CHUNKS; ++c)
-            tma_load_4d(sq + s * F::Q_TILE + c * (128 * 128), &fa.q, c * 64, 0,
-                        at.s.first + at.i * NQ * tq1 + s * tq1, at.h, &f.q_full);
-      }
-      __syncwarp();
-      if constexpr (!E8) {
-        const int limit = line.limit(at.s, at.i), end = at.j + seg;
-        const int shift = PAGED ? fa.box_shift : 7;
-        // lane b: the page of box b of the tile, looked up a tile ahead
-        auto pages_of = [&](int j) {
-          int page = a.c.n_pages;
-          if constexpr (PAGED) {
-            const int key = j * KEYS + (lane << shift);
-            if ((lane << shift) < KEYS && key < limit) {
-              page = a.table[(long long)at.b * a.table_stride + (key >> a.c.page_shift)];
-              if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;
-            }
-          }
-          return page;
-        };
-        auto load = [&](bool v, int j, int pages) {
-          for (int p = 0; p < PARTS; ++p, to.next()) {
-            const int st = to.stage;
-            // (a fresh barrier's phase before the first counts as complete)
-            if (!flash_wait(&f.empty[st], to.lap ^ 1, &f.gave_up)) return false;
-            to.flip(v);
-            uint64_t* full = &f.full[v][st];
-            const int rows = v && F::VK < (1 << shift) ? F::VK : 1 << shift;  // of a box
-            const int n_rows = v ? F::VK : KEYS, cols = v ? CHUNKS : F::KC;
-            if (elect_one()) mbar_arrive_expect_tx(full, F::STAGE);
-            for (int row = 0; row < n_rows; row += rows) {
-              const int key = row + (v ? p * F::VK : 0);  // in the tile
-              const int page = __shfl_sync(0xffffffffu, pages, key >> shift);
-              const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
-                                    : at.s.first + j * KEYS + key;
-              if (elect_one()) {
-                const uint32_t dst = ring + st * F::STAGE + row * 128;
-                for (int c = 0; c < cols; ++c)
-                  tma_load_4d(dst + c * (n_rows * 128), v ? &fa.v : &fa.k,
-                              (c + (v ? 0 : p * F::KC)) * 64, pos, at.h, PAGED ? page : 0, full);
-              }
-              __syncwarp();
-            }
-          }
-          return true;
-        };
-        int now = pages_of(at.j), next = pages_of(at.j + 1 < end ? at.j + 1 : at.j);
-        ok = load(false, at.j, now);
-        for (int j = at.j; ok && j < end; ++j) {
-          if (NQ == 1) {  // scores run a tile ahead of the output
-            if (j + 1 < end) ok = load(false, j + 1, next);
-            ok = ok && load(true, j, now);
-          } else {
-            ok = load(true, j, now);
-            if (j + 1 < end) ok = ok && load(false, j + 1, next);
-          }
-          now = next;
-          next = pages_of(j + 2 < end ? j + 2 : at.j);
-        }
+    if (warp == 0) {
+      // ---- TMA producer: queries, and keys and values unless they are converted
+      Ring<STAGES> to;
+      int seg_no = 0;
+      while (at.left > 0) {
+        const int seg = at.segment(line), ns = streams(at);
+        bool ok = seg_no == 0 || flash_wait(&f.q_empty, (seg_no - 1) & 1, &f.gave_up);
         if (!ok) break;
-      }
-      at.skip(line, seg);
-      make_uniform(at);
-      ++seg_no;
-    }
-    // copies in flight must land before the CTA can end
-    if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f.gave_up);
-    if (!E8)
-      for (int i = 0; i < STAGES; ++i)
-        for (int v = 0; v < 2; ++v) {  // the last load of each kind (of none: complete at once)
-          const uint64_t start = global_ns();
-          while (!mbar_try_wait(&f.full[v][i], (to.phase[v] >> i & 1) ^ 1))
-            if (global_ns() - start > uint64_t(FLASH_WAIT_NS)) break;
-        }
-  } else if (warp <= 2) {
-    // ---- MMA issuers.  Two streams: warp 1 + s issues the scores and outputs of
-    // stream s.  One stream: warp 1 issues the scores, warp 2 the outputs.
-    constexpr uint32_t id_s = idesc_f16(BF, 128, KEYS, false), id_o = idesc_f16(BF, 128, HD, true);
-    const int me = warp - 1;
-    Ring<STAGES> ring_at;
-    int seg_no = 0, cnt = 0, segs = 0;  // segments, own key tiles, own segments so far
-    auto on = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
-    auto issue_s = [&](int slot, int q, int st) {
-      uint64_t qd = desc_k_major(sq + q * F::Q_TILE);
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p, st = on(st)) {
-        uint64_t kd = desc_k_major(ring + st * F::STAGE);
-#pragma unroll
-        for (int c = 0; c < F::KC; ++c, qd += 128 * 128 / 16, kd += KEYS * 128 / 16)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, p + c + k > 0);
-      }
-    };
-    // the weights lie over the scores, those of a half over its own
-    auto weights_at = [](int key) { return key / 2 + (HALVES == 2 && key >= 64 ? 32 : 0); };
-    auto issue_o = [&](int slot, int s, int st, bool more) {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p, st = on(st)) {
-        const uint64_t vd = desc_mn_major(ring + st * F::STAGE, F::VK * 128);
-#pragma unroll
-        for (int k = 0; k < F::VK / 16; ++k)
-          tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + weights_at(p * F::VK + k * 16),
-                    vd + k * (2048 / 16), id_o, more || p + k > 0);
-      }
-    };
-    // Waits for the operand in the ring's next stages and moves past it; its first stage.
-    auto take = [&](int v, int& first) {
-      first = ring_at.stage;
-      bool ok = true;
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p, ring_at.next())
-        ok = ok && flash_wait(&f.full[v][ring_at.stage], ring_at.flip(v), &f.gave_up);
-      return ok;
-    };
-    auto pass = [&] {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p) ring_at.next();
-    };
-    auto release = [&](int st) {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p, st = on(st)) tc_commit(&f.empty[st]);
-    };
-    // Zero what lies behind the sequence in a V tile (both streams' issuers do: zeros
-    // over zeros).
-    auto clear_tail = [&](int st, int j) {
-      if constexpr (!E8) {
-        const int keep = at.s.len - j * KEYS;
-        if (keep >= KEYS) return;
-        for (int p = 0; p < PARTS; ++p, st = on(st))
-          for (int x = lane; x < F::VK * 8; x += 32) {
-            if (x / 8 + p * F::VK < keep) continue;
-            const uint32_t to = ring + st * F::STAGE + x * 16;
-            for (int c = 0; c < CHUNKS; ++c)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + c * F::VK * 128),
-                           "r"(0)
-                           : "memory");
-          }
-        fence_async_smem();
-        __syncwarp();
-      }
-    };
-    bool ok = true;
-    while (at.left > 0 && ok) {
-      const int seg = at.segment(line), end = at.j + seg, ns = streams(at);
-      // (whoever issues scores; the outputs' issuer of one stream may be two segments
-      // behind, where the barrier's parity says nothing)
-      if (NQ == 2 || me == 0)
-        ok = flash_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f.gave_up);
-      int k_at, v_at;
-      if constexpr (NQ == 2) {
-        const bool active = me < ns;
-        const int e = !active ? at.j : me == 0 ? stream_end(at, 0, end) : end;
-        ok = ok && take(0, k_at);
-        if (!ok) break;
-        tc_fence_after();
         if (elect_one()) {
-          if (at.j < e) {
-            issue_s(me, me, k_at);
-            tc_commit(&f.s_full[me]);
-          }
-          release(k_at);
-          if (seg == 1) tc_commit(&f.q_empty);
+          mbar_arrive_expect_tx(&f.q_full, ns * CHUNKS * tile_rows * 128);
+          for (int s = 0; s < ns; ++s)
+            for (int c = 0; c < CHUNKS; ++c)
+              tma_load_4d(sq + s * F::Q_TILE + c * (128 * 128), &fa.q, c * 64, 0,
+                          at.s.first + at.i * NQ * tq1 + s * tq1, at.h, &f.q_full);
         }
-        for (int j = at.j; j < end && ok; ++j) {
-          const bool more = j + 1 < end;
-          ok = take(1, v_at);
+        __syncwarp();
+        if constexpr (!E8) {
+          const int limit = line.limit(at.s, at.i), end = at.j + seg;
+          const int shift = PAGED ? fa.box_shift : 7;
+          // lane b: the page of box b of the tile, looked up a tile ahead
+          auto pages_of = [&](int j) {
+            int page = a.c.n_pages;
+            if constexpr (PAGED) {
+              const int key = j * KEYS + (lane << shift);
+              if ((lane << shift) < KEYS && key < limit) {
+                page = a.table[(long long)at.b * a.table_stride + (key >> a.c.page_shift)];
+                if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;
+              }
+            }
+            return page;
+          };
+          auto load = [&](bool v, int j, int pages) {
+            for (int p = 0; p < PARTS; ++p, to.next()) {
+              const int st = to.stage;
+              // (a fresh barrier's phase before the first counts as complete)
+              if (!flash_wait(&f.empty[st], to.lap ^ 1, &f.gave_up)) return false;
+              to.flip(v);
+              uint64_t* full = &f.full[v][st];
+              const int rows = v && F::VK < (1 << shift) ? F::VK : 1 << shift;  // of a box
+              const int n_rows = v ? F::VK : KEYS, cols = v ? CHUNKS : F::KC;
+              if (elect_one()) mbar_arrive_expect_tx(full, F::STAGE);
+              for (int row = 0; row < n_rows; row += rows) {
+                const int key = row + (v ? p * F::VK : 0);  // in the tile
+                const int page = __shfl_sync(0xffffffffu, pages, key >> shift);
+                const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
+                                      : at.s.first + j * KEYS + key;
+                if (elect_one()) {
+                  const uint32_t dst = ring + st * F::STAGE + row * 128;
+                  for (int c = 0; c < cols; ++c)
+                    tma_load_4d(dst + c * (n_rows * 128), v ? &fa.v : &fa.k,
+                                (c + (v ? 0 : p * F::KC)) * 64, pos, at.h, PAGED ? page : 0, full);
+                }
+                __syncwarp();
+              }
+            }
+            return true;
+          };
+          int now = pages_of(at.j), next = pages_of(at.j + 1 < end ? at.j + 1 : at.j);
+          ok = load(false, at.j, now);
+          for (int j = at.j; ok && j < end; ++j) {
+            if (NQ == 1) {  // scores run a tile ahead of the output
+              if (j + 1 < end) ok = load(false, j + 1, next);
+              ok = ok && load(true, j, now);
+            } else {
+              ok = load(true, j, now);
+              if (j + 1 < end) ok = ok && load(false, j + 1, next);
+            }
+            now = next;
+            next = pages_of(j + 2 < end ? j + 2 : at.j);
+          }
           if (!ok) break;
-          if (j < e) {
-            clear_tail(v_at, j);
-            // O is free once the epilogue of the stream's last segment has read it
-            if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
-            ok = ok && flash_wait(&f.p_full[me], cnt & 1, &f.gave_up);
+        }
+        at.skip(line, seg);
+        make_uniform(at);
+        ++seg_no;
+      }
+      // copies in flight must land before the CTA can end
+      if (seg_no > 0) flash_wait(&f.q_full, (seg_no - 1) & 1, &f.gave_up);
+      if (!E8)
+        for (int i = 0; i < STAGES; ++i)
+          for (int v = 0; v < 2; ++v) {  // the last load of each kind (of none: complete at once)
+            const uint64_t start = global_ns();
+            while (!mbar_try_wait(&f.full[v][i], (to.phase[v] >> i & 1) ^ 1))
+              if (global_ns() - start > uint64_t(FLASH_WAIT_NS)) break;
+          }
+    } else if (warp <= 2) {
+      // ---- MMA issuers.  Two streams: warp 1 + s issues the scores and outputs of
+      // stream s.  One stream: warp 1 issues the scores, warp 2 the outputs.
+      constexpr uint32_t id_s = idesc_f16(BF, 128, KEYS, false), id_o = idesc_f16(BF, 128, HD, true);
+      const int me = warp - 1;
+      Ring<STAGES> ring_at;
+      int seg_no = 0, cnt = 0, segs = 0;  // segments, own key tiles, own segments so far
+      auto on = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
+      auto issue_s = [&](int slot, int q, int st) {
+        uint64_t qd = desc_k_major(sq + q * F::Q_TILE);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p, st = on(st)) {
+          uint64_t kd = desc_k_major(ring + st * F::STAGE);
+#pragma unroll
+          for (int c = 0; c < F::KC; ++c, qd += 128 * 128 / 16, kd += KEYS * 128 / 16)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma(tmem + slot * KEYS, qd + k * 2, kd + k * 2, id_s, p + c + k > 0);
+        }
+      };
+      // the weights lie over the scores, those of a half over its own
+      auto weights_at = [](int key) { return key / 2 + (HALVES == 2 && key >= 64 ? 32 : 0); };
+      auto issue_o = [&](int slot, int s, int st, bool more) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p, st = on(st)) {
+          const uint64_t vd = desc_mn_major(ring + st * F::STAGE, F::VK * 128);
+#pragma unroll
+          for (int k = 0; k < F::VK / 16; ++k)
+            tc_mma_ts(tmem + 256 + s * HD, tmem + slot * KEYS + weights_at(p * F::VK + k * 16),
+                      vd + k * (2048 / 16), id_o, more || p + k > 0);
+        }
+      };
+      // Waits for the operand in the ring's next stages and moves past it; its first stage.
+      auto take = [&](int v, int& first) {
+        first = ring_at.stage;
+        bool ok = true;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p, ring_at.next())
+          ok = ok && flash_wait(&f.full[v][ring_at.stage], ring_at.flip(v), &f.gave_up);
+        return ok;
+      };
+      auto pass = [&] {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) ring_at.next();
+      };
+      auto release = [&](int st) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p, st = on(st)) tc_commit(&f.empty[st]);
+      };
+      // Zero what lies behind the sequence in a V tile (both streams' issuers do: zeros
+      // over zeros).
+      auto clear_tail = [&](int st, int j) {
+        if constexpr (!E8) {
+          const int keep = at.s.len - j * KEYS;
+          if (keep >= KEYS) return;
+          for (int p = 0; p < PARTS; ++p, st = on(st))
+            for (int x = lane; x < F::VK * 8; x += 32) {
+              if (x / 8 + p * F::VK < keep) continue;
+              const uint32_t to = ring + st * F::STAGE + x * 16;
+              for (int c = 0; c < CHUNKS; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + c * F::VK * 128),
+                             "r"(0)
+                             : "memory");
+            }
+          fence_async_smem();
+          __syncwarp();
+        }
+      };
+      bool ok = true;
+      while (at.left > 0 && ok) {
+        const int seg = at.segment(line), end = at.j + seg, ns = streams(at);
+        // (whoever issues scores; the outputs' issuer of one stream may be two segments
+        // behind, where the barrier's parity says nothing)
+        if (NQ == 2 || me == 0)
+          ok = flash_wait(RESCALE_Q ? &f.q_ready : &f.q_full, seg_no & 1, &f.gave_up);
+        int k_at, v_at;
+        if constexpr (NQ == 2) {
+          const bool active = me < ns;
+          const int e = !active ? at.j : me == 0 ? stream_end(at, 0, end) : end;
+          ok = ok && take(0, k_at);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (at.j < e) {
+              issue_s(me, me, k_at);
+              tc_commit(&f.s_full[me]);
+            }
+            release(k_at);
+            if (seg == 1) tc_commit(&f.q_empty);
+          }
+          for (int j = at.j; j < end && ok; ++j) {
+            const bool more = j + 1 < end;
+            ok = take(1, v_at);
             if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              issue_o(me, me, v_at, j > at.j);
-              tc_commit(&f.o_full[me]);
+            if (j < e) {
+              clear_tail(v_at, j);
+              // O is free once the epilogue of the stream's last segment has read it
+              if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
+              ok = ok && flash_wait(&f.p_full[me], cnt & 1, &f.gave_up);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_o(me, me, v_at, j > at.j);
+                tc_commit(&f.o_full[me]);
+                release(v_at);
+              }
+              ++cnt;
+            } else if (elect_one()) {
               release(v_at);
             }
-            ++cnt;
-          } else if (elect_one()) {
-            release(v_at);
+            if (more) {
+              ok = take(0, k_at);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                if (j + 1 < e) {
+                  issue_s(me, me, k_at);
+                  tc_commit(&f.s_full[me]);
+                }
+                release(k_at);
+                if (j + 2 == end) tc_commit(&f.q_empty);
+              }
+            }
           }
-          if (more) {
+          if (active) {
+            // a stream without tiles here keeps step with its epilogues all the same
+            if (ok && e <= at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
+            ++segs;
+          }
+        } else if (me == 0) {
+          for (int x = 0; x < seg && ok; ++x, ++cnt) {
             ok = take(0, k_at);
+            // the scores' columns are free once the output has used the weights in them
+            if (ok && cnt > 1) ok = flash_wait(&f.o_full[cnt & 1], ((cnt >> 1) - 1) & 1, &f.gave_up);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              if (j + 1 < e) {
-                issue_s(me, me, k_at);
-                tc_commit(&f.s_full[me]);
-              }
+              issue_s(cnt & 1, 0, k_at);
+              tc_commit(&f.s_full[cnt & 1]);
               release(k_at);
-              if (j + 2 == end) tc_commit(&f.q_empty);
+              if (x + 1 == seg) tc_commit(&f.q_empty);
+            }
+            if (x > 0) pass();         // the V tile behind it
+            if (x + 1 == seg) pass();  // the last one
+          }
+        } else {
+          pass();  // the first K tile
+          for (int j = at.j; j < end && ok; ++j, ++cnt) {
+            if (j + 1 < end) pass();
+            ok = take(1, v_at);
+            if (!ok) break;
+            clear_tail(v_at, j);
+            if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[0], (segs - 1) & 1, &f.gave_up);
+            ok = ok && flash_wait(&f.p_full[cnt & 1], (cnt >> 1) & 1, &f.gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_o(cnt & 1, 0, v_at, j > at.j);
+              tc_commit(&f.o_full[cnt & 1]);
+              release(v_at);
             }
           }
-        }
-        if (active) {
-          // a stream without tiles here keeps step with its epilogues all the same
-          if (ok && e <= at.j && segs > 0) ok = flash_wait(&f.o_empty[me], (segs - 1) & 1, &f.gave_up);
           ++segs;
         }
-      } else if (me == 0) {
-        for (int x = 0; x < seg && ok; ++x, ++cnt) {
-          ok = take(0, k_at);
-          // the scores' columns are free once the output has used the weights in them
-          if (ok && cnt > 1) ok = flash_wait(&f.o_full[cnt & 1], ((cnt >> 1) - 1) & 1, &f.gave_up);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_s(cnt & 1, 0, k_at);
-            tc_commit(&f.s_full[cnt & 1]);
-            release(k_at);
-            if (x + 1 == seg) tc_commit(&f.q_empty);
-          }
-          if (x > 0) pass();         // the V tile behind it
-          if (x + 1 == seg) pass();  // the last one
-        }
-      } else {
-        pass();  // the first K tile
-        for (int j = at.j; j < end && ok; ++j, ++cnt) {
-          if (j + 1 < end) pass();
-          ok = take(1, v_at);
-          if (!ok) break;
-          clear_tail(v_at, j);
-          if (j == at.j && segs > 0) ok = flash_wait(&f.o_empty[0], (segs - 1) & 1, &f.gave_up);
-          ok = ok && flash_wait(&f.p_full[cnt & 1], (cnt >> 1) & 1, &f.gave_up);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_o(cnt & 1, 0, v_at, j > at.j);
-            tc_commit(&f.o_full[cnt & 1]);
-            release(v_at);
-          }
-        }
-        ++segs;
+        at.skip(line, seg);
+        make_uniform(at);
+        ++seg_no;
       }
-      at.skip(line, seg);
-      make_uniform(at);
-      ++seg_no;
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else if (warp < 4 + F::SOFT_WARPS) {
     // ---- softmax and epilogue.  Two streams: a thread for each row of its warpgroup's
     // stream.  (Two threads a row, 64 keys each, made the streams run in step, both at

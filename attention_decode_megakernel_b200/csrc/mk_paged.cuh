@@ -8,10 +8,13 @@
 // private ring of stages in shared memory: one lane asks TMA for the 16 rows
 // of K and of V, a box of (128 bytes, 16 positions, columns of 128 bytes) in the
 // 128-byte swizzle, and looks the next page up a step ahead.  (16-byte cp.async copies
-// by all lanes were a quarter of the instructions.)  A warp is bound by the latency of its
-// instructions, four cycles each, so rows of up to 256 bytes, whose stages leave room,
-// have eight warps (64 sequences over an e4m3 cache at head_dim 256: 49 us with
-// four); rows of 512 bytes have four.  No barrier joins the warps
+// by all lanes were a quarter of the instructions.)  Rows of up to 256 bytes, whose
+// stages leave room, have eight warps (64 sequences over an e4m3 cache at head_dim 256:
+// 36.6 us, 49 with four and 38.6 with twelve); rows of 512 bytes have four.  Between the
+// first load and the last the copies run at the memory's rate (the same 64 sequences at
+// head_dim 128 and 256 in bf16: 162 MB more in 24.5 us); more chains of products, fewer
+// conversions or loads change nothing.  What is left is around them: finding the shares,
+// first loads, joining warps and partials, 10 us.  No barrier joins the warps
 // until the unit ends, and the ring runs ahead into the next unit.
 //
 // The products run on mma.m16n8k16 with the keys as M: S^T = K Q^T and

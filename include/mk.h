@@ -432,8 +432,9 @@ int mk_qk_norm_rope(const mk_rope *rope, const void *q, int64_t q_ts,
  * head * head_stride + position * pos_stride values into k and into v, 16-byte
  * aligned; rows do not overlap.  dtype MK_BF16 or MK_FP16, or MK_E4M3 with one
  * float scale for each row in k_scale and v_scale (16-byte aligned),
- * [page][head][position] without gaps: a row's values are code * scale.  Scales are positive, normal
- * numbers; mk_kv_write stores powers of two from 2^-64 to 2^120.  An engine's
+ * [page][head][position] without gaps: a row's values are code * scale.
+ * Scales are positive, normal numbers; mk_kv_write stores powers of two from
+ * 2^-64 to 2^120.  An engine's
  * cache as mk_get_state copies it out is one sequence of such pages (page
  * stride page_size * head_dim, head stride pos * head_dim) when its length is
  * a multiple of the page. */
@@ -495,7 +496,8 @@ size_t mk_attn_ws_bytes(int head_dim);
  * What lies behind seq_lens[b] in a page is never part of a result, whatever
  * its bits; a key that a token does not see within seq_lens[b] must have
  * finite values.  out must not overlap an input.  Results do not depend on
- * timing: the same call gives the same bits. */
+ * timing: the same call gives the same bits.  Device-side waits are bounded
+ * (2 s): rows of a tile whose wait runs out are set to NaN. */
 int mk_attn_paged(const mk_kv_cache *cache, const void *q, int64_t q_ts,
                   int64_t q_hs, const int32_t *block_table, int table_stride,
                   const int32_t *seq_lens, const int32_t *cu_q, void *out,

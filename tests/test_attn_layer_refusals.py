@@ -115,6 +115,7 @@ def _cache(**k):
 BAD_CACHES = [
     (dict(k=None), 1), (dict(v=None), 1), (dict(k=P + 8), 1), (dict(v=P + 4), 1),
     (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(k_scale=P + 2), 1),
+    (dict(k_scale=P + 4), 1), (dict(v_scale=P + 8), 1),
     (dict(page_stride=-2048), 1), (dict(page_stride=2047), 1), (dict(head_stride=1000), 1),
     (dict(pos_stride=72), 1), (dict(pos_stride=32), 1), (dict(head_stride=0), 1),
     (dict(page_stride=0), 1), (dict(n_pages=0), 1), (dict(kv_heads=0), 1), (dict(page_size=0), 1),
