@@ -10,7 +10,7 @@
 // 128-byte swizzle, and looks the next page up a step ahead.  (16-byte cp.async copies
 // by all lanes were a quarter of the instructions.)  Rows of up to 256 bytes, whose
 // stages leave room, have eight warps (64 sequences over an e4m3 cache at head_dim 256:
-// 36.6 us, 49 with four and 38.6 with twelve); rows of 512 bytes have four.  Between the
+// 36 us, 49 with four and 38.6 with twelve); rows of 512 bytes have four.  Between the
 // first load and the last the copies run at the memory's rate (the same 64 sequences at
 // head_dim 128 and 256 in bf16: 162 MB more in 24.5 us); more chains of products, fewer
 // conversions or loads change nothing.  What is left is around them: finding the shares,
@@ -65,8 +65,10 @@ struct FewCfg {
   static constexpr int KEYS = 16 * WARPS;        // of a tile: 16 a warp
   static constexpr int STAGE = 32 * ROW, SCALES = E8 ? 128 : 0;  // 16 keys, 16 values; their scales
   static constexpr int ROWS = 8 * NT;
-  static constexpr int SLOTS = WARPS == 8 ? 3 : 2;  // of the join: so many warps at a time
-  static constexpr int JOIN = SLOTS * ROWS * (HD + 4) * 4 + SLOTS * ROWS * 8;
+  // The join: all warps' values of 8 rows and so many columns, then {maximum, sum} of each
+  // warp's rows and of the rows themselves.
+  static constexpr int COLS = WARPS == 8 && ROW * NT >= 256 ? 64 : HD < 128 ? HD : 128;
+  static constexpr int JOIN = WARPS * 8 * (COLS + 4) * 4 + (WARPS + 1) * ROWS * 8;
   static constexpr int FIT = (227 * 1024 - int(sizeof(FewBars<WARPS>)) - JOIN) /
                              (WARPS * (STAGE + SCALES));
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -208,8 +210,10 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
   const int per = f.per;
   const uint32_t ring = smem_addr(smem) + warp * (STAGES * F::STAGE);
   const uint32_t scales = smem_addr(smem) + F::RING + warp * (STAGES * F::SCALES);
-  float* join_o = reinterpret_cast<float*>(join);  // [slot][ROWS][HD + 4]
-  float2* join_ml = reinterpret_cast<float2*>(join + F::SLOTS * ROWS * (HD + 4) * 4);
+  constexpr int COLS = F::COLS;
+  float* join_o = reinterpret_cast<float*>(join);  // [warp][8][COLS + 4]
+  float2* join_ml = reinterpret_cast<float2*>(join + WARPS * 8 * (COLS + 4) * 4);
+  float2* join_row = join_ml + WARPS * ROWS;
 
   // The page of this warp's keys at `ahead`; n_pages, which lies outside the maps and
   // arrives as zeros, for one outside the cache.
@@ -481,7 +485,10 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
       at.skip(line, 1);
     }
 
-    // ---- join the warps, some of them at a time, and write the segment
+    // ---- join the warps and write the segment: the rows' maxima first, then the sums of
+    // all warps' values, 8 rows by COLS columns at a time, in the warps' order (half of the
+    // warps left theirs to the other half in turn before: one token over 520 keys took 7.5
+    // us instead of 7.0, 300 sequences of up to 300 43.4 instead of 41.1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -490,18 +497,51 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 8);
         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 16);
         if (*(volatile int*)&f.gave_up) l[nt][x] = m[nt][x] = __int_as_float(0x7FC00000);
+        if (g == 0) join_ml[warp * ROWS + nt * 8 + 2 * t + x] = make_float2(m[nt][x], l[nt][x]);
       }
-    // this lane's values, to slot w
-    auto leave = [&](int w) {
+    __syncthreads();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+          top = fmaxf(top, join_ml[w * ROWS + nt * 8 + 2 * t + x].x);
+        const float f0 = ex2(m[nt][x] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          o[nt][i][x] *= f0;
+          o[nt][i][2 + x] *= f0;
+        }
+      }
+    if (threadIdx.x < ROWS) {
+      const int r = threadIdx.x;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, join_ml[w * ROWS + r].x);
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 ml = join_ml[w * ROWS + r];
+        sum += ex2(ml.x - base) * ml.y;
+      }
+      join_row[r] = make_float2(top, sum);
+    }
+    const bool whole = u.j == 0 && seg == u.n;
+    const int tokens = u.s.n_new - u.i * tq, live = (tokens < tq ? tokens : tq) * a.group;
+    const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int d0 = 0; d0 < HD; d0 += COLS) {
+        if (nt + d0 > 0) __syncthreads();  // the last columns have been read
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int r = nt * 8 + 2 * t + x;
-          if (g == 0) join_ml[w * ROWS + r] = make_float2(m[nt][x], l[nt][x]);
-          float* to = join_o + (w * ROWS + r) * (HD + 4);
+          if (nt * 8 + 2 * t + x >= live) continue;
+          float* to = join_o + (warp * 8 + 2 * t + x) * (COLS + 4) - d0;
 #pragma unroll
-          for (int i = 0; i < STEPS; ++i) {
+          for (int i = d0 / 16; i < (d0 + COLS) / 16; ++i) {
             if constexpr (E8) {
               *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
                   make_float2(o[nt][i][x], o[nt][i][2 + x]);
@@ -511,83 +551,40 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
             }
           }
         }
-    };
+        __syncthreads();
+        for (int x = threadIdx.x; x < 8 * (COLS / 4); x += F::THREADS) {
+          const int at8 = x / (COLS / 4), r = nt * 8 + at8, col = x % (COLS / 4) * 4;
+          const int d = d0 + col;
+          if (r >= live) break;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int held = WARPS; held > F::SLOTS;) {  // warps that still hold something
-      const int n = held / 2 < F::SLOTS ? held / 2 : F::SLOTS;
-      if (warp >= held - n && warp < held) leave(warp - (held - n));
-      __syncthreads();
-      const int mine = warp - (held - 2 * n);
-      if (mine >= 0 && mine < n) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int r = nt * 8 + 2 * t + x;
-            const float2 ml = join_ml[mine * ROWS + r];
-            const float top = fmaxf(m[nt][x], ml.x), base = top == -INFINITY ? 0.f : top;
-            const float f0 = ex2(m[nt][x] - base), f1 = ex2(ml.x - base);
-            const float* from = join_o + (mine * ROWS + r) * (HD + 4);
-            l[nt][x] = l[nt][x] * f0 + ml.y * f1;
-            m[nt][x] = top;
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-              float2 y;
-              if constexpr (E8)
-                y = *reinterpret_cast<const float2*>(from + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
-              else
-                y = make_float2(from[16 * i + g], from[16 * i + 8 + g]);
-              o[nt][i][x] = o[nt][i][x] * f0 + y.x * f1;
-              o[nt][i][2 + x] = o[nt][i][2 + x] * f0 + y.y * f1;
-            }
+          for (int w = 0; w < WARPS; ++w) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(join_o + (w * 8 + at8) * (COLS + 4) + col);
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
           }
+          const float2 ml = join_row[r];
+          if (whole) {
+            const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
+            const int head = u.h * a.group + r % a.group, token = u.i * tq + r / a.group;
+            uint2 w;
+            w.x = RowType<T>::pack2(acc.x * inv, acc.y * inv);
+            w.y = RowType<T>::pack2(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(a.out + ((long long)(u.s.first + token) * a.o_ts +
+                                               head * a.o_hs + d) * 2) = w;
+            if (a.lse && d == 0)
+              a.lse[(long long)(u.s.first + token) * a.q_heads + head] = row_lse(ml.x, ml.y);
+          } else {
+            *reinterpret_cast<float4*>(part.o + (slot * ROWS + r) * HD + d) = acc;
+            if (d == 0) part.ml[slot * ROWS + r] = ml;
+          }
+        }
       }
-      held -= n;
-      __syncthreads();
-    }
-    if (warp < F::SLOTS) leave(warp);
-    __syncthreads();
-    const bool whole = u.j == 0 && seg == u.n;
-    const size_t slot = 2 * size_t(blockIdx.x) + (u.j == 0 ? 1 : 0);
-    for (int x = threadIdx.x; x < ROWS * (HD / 4); x += F::THREADS) {
-      const int r = x / (HD / 4), d = x % (HD / 4) * 4, token = u.i * tq + r / a.group;
-      if (r >= tq * a.group || token >= u.s.n_new) continue;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < F::SLOTS; ++w) top = fmaxf(top, join_ml[w * ROWS + r].x);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < F::SLOTS; ++w) {
-        const float2 ml = join_ml[w * ROWS + r];
-        const float f = ex2(ml.x - base);
-        const float4 y = *reinterpret_cast<const float4*>(join_o + (w * ROWS + r) * (HD + 4) + d);
-        sum += f * ml.y;
-        acc.x += f * y.x;
-        acc.y += f * y.y;
-        acc.z += f * y.z;
-        acc.w += f * y.w;
-      }
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        const int head = u.h * a.group + r % a.group;
-        uint2 w;
-        w.x = RowType<T>::pack2(acc.x * inv, acc.y * inv);
-        w.y = RowType<T>::pack2(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(a.out + ((long long)(u.s.first + token) * a.o_ts +
-                                           head * a.o_hs + d) * 2) = w;
-        if (a.lse && d == 0)
-          a.lse[(long long)(u.s.first + token) * a.q_heads + head] = row_lse(top, sum);
-      } else {
-        *reinterpret_cast<float4*>(part.o + (slot * ROWS + r) * HD + d) = acc;
-        if (d == 0) part.ml[slot * ROWS + r] = make_float2(top, sum);
-      }
-    }
     if (u.j == 0 && !whole && threadIdx.x == 0) {
-      const int tokens = u.s.n_new - u.i * tq;
-      Left left = {(u.n - seg + per - 1) / per, u.s.first + u.i * tq, u.h,
-                   (tokens < tq ? tokens : tq) * a.group};
+      Left left = {(u.n - seg + per - 1) / per, u.s.first + u.i * tq, u.h, live};
       part.left[blockIdx.x] = left;
     }
     __syncthreads();  // the join buffer is free again

@@ -174,7 +174,11 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
   const int lane = threadIdx.x & 31;
   long long total = 0, head = 0;  // length of a head of the lane's sequence
   Seq s = {};
+  // Sequences in rounds of 32; lane x keeps the place where round x * stride starts.
+  const int stride = (a.batch + 1023) / 1024;
+  long long start_of = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    if (b0 / 32 == lane * stride) start_of = total;
     head = 0;
     if (b0 + lane < a.batch) {
       s = seq_of(a, b0 + lane);
@@ -191,8 +195,12 @@ __device__ __forceinline__ Cursor<KT> find_share(const Line<KT>& line, int cta, 
   if (at >= total) return c;
   c.left = int(total - at < per ? total - at : per);
   // the sequence that holds place `at`
-  long long before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+  // (searched from the first round, 300 short sequences took 41.1 us instead of 39.6, 2300
+  // 202 instead of 174)
+  const int from = 31 - __clz(__ballot_sync(
+                            0xffffffffu, lane * stride * 32 < a.batch && start_of <= at));
+  long long before = __shfl_sync(0xffffffffu, start_of, from);
+  for (int b0 = from * stride * 32; b0 < a.batch; b0 += 32) {
     if (a.batch > 32) {
       head = 0;
       if (b0 + lane < a.batch) {

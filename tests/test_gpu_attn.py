@@ -409,6 +409,16 @@ def test_many_sequences(mk):
     run_packed(mk, gen, [i % 9 for i in range(700)], 2, 1, 64, BF)
 
 
+@pytest.mark.parametrize("kind", [BF, E4])
+def test_more_sequences_than_a_warp_remembers(mk, kind):
+    """2100 sequences, runs of empty ones among them: shares found from two rounds each on."""
+    gen = torch.Generator(device="cuda").manual_seed(48)
+    new = [0 if 900 < i < 1400 or i % 50 == 7 else 1 + (i % 700 == 0) for i in range(2100)]
+    lens = [(7 * i) % 90 if n else 0 for i, n in enumerate(new)]
+    run_paged(mk, gen, new, lens, 2, 1, 64, 16, BF, kind)
+    run_paged(mk, gen, [9 * n for n in new], [n + 9 for n in lens], 4, 1, 64, 16, BF, kind)
+
+
 def test_nothing_to_do(mk):
     pool, table, _ = make_paged(torch.Generator(device="cuda").manual_seed(1), [5], 1, 64, 16, BF)
     q = torch.zeros(4, 2, 64, dtype=BF, device="cuda")
