@@ -61,14 +61,16 @@ int device_sms(int* dev, int* sms) {
 // What a unit costs besides its key tiles, in key tiles (mk_split.cuh), by sweeps: two
 // for tiles of rows (8 prompts of up to 4096 tokens at head_dim 128: 385 us at 0, 366 at 1,
 // 364 at 2, 377 at 4), two for few rows (64 sequences of up to 4096 over an e4m3 cache:
-// 51.3 us at 0, 50.2 at 1, 49.2 at 2 and more).
+// 39.6 us at 0, 38.4 at 1, 36.0 at 2, 35.7 at 3, 36.2 at 4; at head_dim 128 31.3, 30.4, 28.7,
+// 29.3, 30.2).
 constexpr int kFewExtra = 2, kFlashExtra = 2;
 
 // Calls whose sequences hold at most so many keys do not divide units over CTAs, and
 // have no join. Measured whole / divided (head_dim 256, 8 + 2 heads): one prompt of 520
-// tokens 13.9 / 15.4 us, of 780 17.3 / 17.0; 5 tokens over 128 keys 8.6 / 11.9, over 260
-// 11.8 / 12.3, over 520 15.5 / 12.2; one token over 64 keys 5.6 / 6.5, over 128 6.6 / 6.9,
-// over 260 9.4 / 7.4.
+// tokens 13.8 / 15.4 us, of 780 17.1 / 17.0; 5 tokens over 128 keys 8.7 / 12.0, over 260
+// 11.8 / 12.4, over 520 15.5 / 12.3; one token over 64 keys 5.1 / 7.1, over 128 6.1 / 6.9,
+// over 260 9.0 / 7.2.  (64 sequences of exactly 520 would gain too, 14.6 / 17.5, but not
+// ragged ones, and the call knows no more than the longest.)
 constexpr int kWholePrompt = 640, kWholeChunk = 256, kWholeFew = 128;
 
 // cuTensorMapEncodeTiled through the runtime (no link against the driver library).
