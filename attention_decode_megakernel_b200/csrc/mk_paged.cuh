@@ -397,8 +397,11 @@ __global__ void __launch_bounds__(FewCfg<C, HD, NT>::THREADS, 1)
           for (int y = 0; y < 2; ++y) {
             kc[y] = __uint_as_float(lds32(scales + stage * 128 + (g + 8 * y) * 4));
             float sv = __uint_as_float(lds32(scales + stage * 128 + 64 + (g + 8 * y) * 4));
-            if (strange >> stage & 1) kc[y] = sv = 1.f;  // zeros, whose scales were not read
-            sv = sv > 0.f ? sv : 1.f;                    // behind the sequence: masked
+            // zeros, whose scales were not read, and what the page holds behind the
+            // sequence: any bits, by the key's place and not by their value (the reciprocal
+            // of a subnormal is infinite, and a weight of 0 times that NaN)
+            if ((strange >> stage & 1) || key + g + 8 * y >= u.s.len) kc[y] = sv = 1.f;
+            sv = sv > 0.f ? sv : 1.f;  // (no row's scale may be otherwise)
             vl[y] = lg2(sv);
             vi[y] = rcp(sv);
           }
