@@ -636,7 +636,8 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     q [rows][q_heads][head_dim] are the newest of sequence b's seq_lens[b] keys,
     which lie in the pages block_table[b] (int32).  out as q; lse float32
     [rows][q_heads] or None; scale head_dim ** -0.5 by default.  Rows behind
-    cu_q[-1] stay as they were."""
+    cu_q[-1] stay as they were.  An expanded q is taken for few rows only (see
+    mk_attn_paged in include/mk.h)."""
     if scale is None:
         scale = cache.head_dim ** -0.5
     if stream is None and workspace is not None and _paged_call.quick(
@@ -662,7 +663,8 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
 def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, stream=None):
     """Causal attention of whole prompts packed one after another: rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [rows][q_heads][head_dim] and of k, v
-    [rows][kv_heads][head_dim] are sequence b."""
+    [rows][kv_heads][head_dim] are sequence b.  k and v may be expanded over their
+    heads; q may not be expanded."""
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if stream is None and workspace is not None and _packed_call.quick(

@@ -40,6 +40,12 @@ int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, vo
   return MK_OK;
 }
 
+// The tensor maps of the many-row kernel walk the tokens and heads of q, and the tokens of
+// packed keys and values: a distance of 0 between several is not theirs.
+bool walked(int64_t ts, int rows, int64_t hs = 1, int heads = 1) {
+  return (ts > 0 || rows == 1) && (hs > 0 || heads == 1);
+}
+
 constexpr int kMaxDevices = 64;
 
 // The current device and its number of multiprocessors.
@@ -95,13 +101,13 @@ EncodeFn encode_tiled() {
 
 // A 4D view of 16-bit values, strides in values for the dims 1 .. 3, boxes of
 // 64 values by b1 by b2, in the 128-byte swizzle; outside the view reads as zero.
+// A stride of 0 is no map's: only a dim of one, which is never walked, may have it.
 bool encode_map(CUtensorMap* m, const void* base, bool bf16, long long d0, long long d1,
                 long long d2, long long d3, long long s1, long long s2, long long s3, int b1,
                 int b2) {
   const EncodeFn fn = encode_tiled();
-  if (!fn) return false;
+  if (!fn || (s1 <= 0 && d1 > 1) || (s2 <= 0 && d2 > 1) || (s3 <= 0 && d3 > 1)) return false;
   const cuuint64_t dims[4] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2), cuuint64_t(d3)};
-  // the stride of a dim of one is never walked; zero is not a valid one
   const cuuint64_t strides[3] = {s1 > 0 ? cuuint64_t(s1) * 2 : 16, s2 > 0 ? cuuint64_t(s2) * 2 : 16,
                                  s3 > 0 ? cuuint64_t(s3) * 2 : 16};
   const cuuint32_t box[4] = {64u, cuuint32_t(b1), cuuint32_t(b2), 1u}, step[4] = {1u, 1u, 1u, 1u};
@@ -184,6 +190,7 @@ int launch_flash(const mk::at::AttnArgs& a, long long longest, void* ws, int dev
   fa.least = 1;
   fa.whole = longest <= (PAGED ? kWholeChunk : kWholePrompt);
   fa.box_shift = 7;
+  fa.k_head = fa.v_head = ~0;
   if (!encode_map(&fa.q, a.q, BF, HD, a.group, a.rows, a.kv_heads, a.q_hs, a.q_ts,
                   a.group * a.q_hs, a.group, fa.tq1))
     return MK_ERR_UNSUPPORTED;
@@ -197,9 +204,13 @@ int launch_flash(const mk::at::AttnArgs& a, long long longest, void* ws, int dev
            encode_map(&fa.v, a.c.v, BF, HD, a.c.page_size, a.c.kv_heads, a.c.n_pages,
                       a.c.pos_stride, a.c.head_stride, a.c.page_stride, vb, 1);
     } else {
-      ok = encode_map(&fa.k, a.k, BF, HD, a.rows, a.kv_heads, 1, a.k_ts, a.k_hs, 0, mk::at::KEYS,
-                      1) &&
-           encode_map(&fa.v, a.v, BF, HD, a.rows, a.kv_heads, 1, a.v_ts, a.v_hs, 0, F::VK, 1);
+      // heads that share their rows (a distance of 0) are one head to the map
+      fa.k_head = a.k_hs ? ~0 : 0;
+      fa.v_head = a.v_hs ? ~0 : 0;
+      ok = encode_map(&fa.k, a.k, BF, HD, a.rows, a.k_hs ? a.kv_heads : 1, 1, a.k_ts, a.k_hs, 0,
+                      mk::at::KEYS, 1) &&
+           encode_map(&fa.v, a.v, BF, HD, a.rows, a.v_hs ? a.kv_heads : 1, 1, a.v_ts, a.v_hs, 0,
+                      F::VK, 1);
     }
     if (!ok) return MK_ERR_UNSUPPORTED;
   } else {
@@ -241,6 +252,8 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   if (!block_table || !aligned(block_table, 4) || table_stride <= 0 || !seq_lens ||
       !aligned(seq_lens, 4))
     return MK_ERR_ARG;
+  const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
+  if (unit > 16 && !walked(q_ts, rows, q_hs, q_heads)) return MK_ERR_UNSUPPORTED;
   a.table = block_table;
   a.table_stride = table_stride;
   a.seq_lens = seq_lens;
@@ -249,7 +262,6 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   if (rc != MK_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long longest = (long long)table_stride * cache->page_size;
-  const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
   by_half_type(dtype, [&](auto t) {
     by_head_dim(cache->head_dim, [&](auto d) {
       using T = typename decltype(t)::type;
@@ -279,6 +291,8 @@ int mk_attn_packed(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int
                      kv_heads, head_dim, scale, dtype, workspace, ws_bytes, &a);
   if (rc != MK_OK || rows == 0 || batch == 0) return rc;
   if (!rows_ok(k, k_ts, k_hs, 2) || !rows_ok(v, v_ts, v_hs, 2)) return MK_ERR_ARG;
+  if (!walked(q_ts, rows, q_hs, q_heads) || !walked(k_ts, rows) || !walked(v_ts, rows))
+    return MK_ERR_UNSUPPORTED;
   a.k = static_cast<const unsigned char*>(k);
   a.v = static_cast<const unsigned char*>(v);
   a.k_ts = k_ts;

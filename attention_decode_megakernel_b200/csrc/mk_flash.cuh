@@ -116,6 +116,7 @@ struct FlashArgs {
   int tq1;              // tokens of a row tile
   int box_shift;        // log2 of the positions of a K box
   int extra, least, whole;  // of the line (mk_split.cuh)
+  int k_head, v_head;       // packed: a key head's place in k, v is `head & this`
 };
 
 // Called by whole warps; the answer is the same in every lane.
@@ -320,13 +321,14 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
               for (int row = 0; row < n_rows; row += rows) {
                 const int key = row + (v ? p * F::VK : 0);  // in the tile
                 const int page = __shfl_sync(0xffffffffu, pages, key >> shift);
+                const int head = PAGED ? at.h : at.h & (v ? fa.v_head : fa.k_head);
                 const int pos = PAGED ? (j * KEYS + key) & (a.c.page_size - 1)
                                       : at.s.first + j * KEYS + key;
                 if (elect_one()) {
                   const uint32_t dst = ring + st * F::STAGE + row * 128;
                   for (int c = 0; c < cols; ++c)
                     tma_load_4d(dst + c * (n_rows * 128), v ? &fa.v : &fa.k,
-                                (c + (v ? 0 : p * F::KC)) * 64, pos, at.h, PAGED ? page : 0, full);
+                                (c + (v ? 0 : p * F::KC)) * 64, pos, head, PAGED ? page : 0, full);
                 }
                 __syncwarp();
               }

@@ -369,7 +369,9 @@ int mk_gemv_w4(const void *codes, const float *scales, const float *x, int T,
  *
  * Rows are [token][head][dim] with the dims of a head side by side; `ts` and
  * `hs` are the distances between tokens and between heads in values (>= 0),
- * so that a slice of a fused projection's output is a valid argument.  Rows
+ * so that a slice of a fused projection's output is a valid argument, and with
+ * a distance of 0 an input whose tokens or heads share rows (but for what the
+ * attention calls say of it).  Rows
  * start on 16-byte boundaries (base pointers and both distances; else
  * MK_ERR_ARG).  head_dim is 64, 128 or 256 (else MK_ERR_UNSUPPORTED).  A call
  * with no tokens (or an empty batch) does nothing. */
@@ -484,7 +486,10 @@ size_t mk_attn_ws_bytes(int head_dim);
  *   q, out [rows][q_heads][head_dim] device, dtype MK_BF16 or MK_FP16; query
  *     head h reads key head h / (q_heads / kv_heads); q_heads a multiple of
  *     the cache's kv_heads, 128 times at most (else MK_ERR_UNSUPPORTED); the
- *     cache of the same dtype or MK_E4M3
+ *     cache of the same dtype or MK_E4M3; a distance of 0 between several
+ *     tokens or heads of q only while q_heads / kv_heads times the new tokens
+ *     of a sequence (rows / batch, rounded up) is 16 or less (else
+ *     MK_ERR_UNSUPPORTED)
  *   block_table device int32 [batch][table_stride]; seq_lens device int32
  *     [batch], held to 0 .. table_stride * page_size (and to 2^30); a page
  *     number outside the cache stands for keys and values of zero
@@ -509,7 +514,9 @@ int mk_attn_paged(const mk_kv_cache *cache, const void *q, int64_t q_ts,
  * results table: prompt processing; kernel bullet list: causal softmax):
  * sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q, k and v,
  * and its row t sees the rows 0 .. t.  k, v [rows][kv_heads][head_dim] device
- * of q's dtype; everything else as mk_attn_paged. */
+ * of q's dtype; everything else as mk_attn_paged.  Heads of k and of v may share
+ * their rows (k_hs or v_hs 0); tokens of k and v and tokens or heads of q that
+ * do are MK_ERR_UNSUPPORTED. */
 int mk_attn_packed(const void *q, int64_t q_ts, int64_t q_hs, const void *k,
                    int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
                    int64_t v_hs, const int32_t *cu_seqlens, void *out,

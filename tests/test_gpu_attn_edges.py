@@ -51,3 +51,63 @@ def test_scales_behind_a_sequence(mk, behind, dtype, hd, t):
                           rows[b][2])
         ref.check(out[at], want[0], want[2], "out of sequence %d" % b)
         ref.check(lse[at], want[1], want[3], "lse of sequence %d" % b)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd,n", [(64, 300), (128, 700), (256, 145)])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+def test_packed_keys_that_share_heads(mk, dtype, hd, n, which):
+    """Keys or values expanded over their heads give the bits of their contiguous copies."""
+    gen = torch.Generator(device="cuda").manual_seed(hd)
+    q, k, v = (torch.randn(n, h, hd, generator=gen, device="cuda").to(dtype) for h in (8, 4, 4))
+    if "k" in which:
+        k = k[:, 1:2].expand(-1, 4, -1)
+    if "v" in which:
+        v = v[:, 2:3].expand(-1, 4, -1)
+    cu = torch.tensor([0, n // 3, n], **I32)
+    got, want = torch.empty_like(q), torch.empty_like(q)
+    lse = [torch.empty(n, 8, device="cuda") for _ in "ab"]
+    mk.attn_packed(q, k, v, cu, got, lse=lse[0])
+    mk.attn_packed(q, k.contiguous(), v.contiguous(), cu, want, lse=lse[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(*lse)
+    for at in (slice(0, n // 3), slice(n // 3, n)):
+        x = ref.attend(q[at].cpu().double(), k[at].cpu().double(), v[at].cpu().double(),
+                       list(range(1, at.stop - at.start + 1)), hd ** -0.5, dtype, dtype)
+        ref.check(got[at], x[0], x[2], "out")
+
+
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("heads", [4, 8])
+def test_paged_queries_that_share_rows(mk, kind, hd, heads):
+    """Queries expanded over heads, tokens or both: the bits of their contiguous copies
+    while a unit has 16 rows or less, a refusal that writes nothing beyond."""
+    gen = torch.Generator(device="cuda").manual_seed(hd)
+    lens, t = [40, 300], 4
+    pool, table, _ = make_paged(gen, lens, 2, hd, 16, kind)
+    cache, sl = mk.KvCache(*pool), torch.tensor(lens, **I32)
+    base = torch.randn(2 * t, heads, hd, generator=gen, device="cuda").to(BF)
+    cu = torch.tensor([0, t, 2 * t], **I32)
+    for q in (base[:, 3:4].expand(-1, heads, -1), base[5:6].expand(2 * t, -1, -1),
+              base[:1, :1].expand(2 * t, heads, -1)):
+        got, want = (torch.full((2 * t, heads, hd), math.nan, dtype=BF, device="cuda")
+                     for _ in "ab")
+        mk.attn_paged(q, cache, table, sl, cu, got)
+        mk.attn_paged(q.contiguous(), cache, table, sl, cu, want)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)  # (and so no NaN that was there before)
+        got.fill_(7)
+        rows = torch.tensor([0, 2 * t], **I32)  # one sequence: units of 16 or 32 rows
+        if heads == 4:
+            mk.attn_paged(q, cache, table[1:], sl[1:], rows, got)
+            mk.attn_paged(q.contiguous(), cache, table[1:], sl[1:], rows, want)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        else:
+            with pytest.raises(mk.MkError):
+                mk.attn_paged(q, cache, table[1:], sl[1:], rows, got)
+            with pytest.raises(mk.MkError):
+                mk.attn_packed(q, q[:, :2], q[:, :2], rows, got)
+            torch.cuda.synchronize()
+            assert bool((got == 7).all())
