@@ -18,8 +18,8 @@ int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, vo
   if (q_heads / kv_heads > 128) return MK_ERR_UNSUPPORTED;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return MK_ERR_ARG;
   if (rows == 0 || batch == 0) return MK_OK;
-  if (!rows_ok(q, q_ts, q_hs, 2) || !rows_ok(out, o_ts, o_hs, 2) || !cu_q || !aligned(cu_q, 4) ||
-      (lse && !aligned(lse, 4)))
+  if (!rows_ok(q, q_ts, q_hs, 2) || !out_rows_ok(out, o_ts, o_hs, rows, q_heads, head_dim, 2) ||
+      !cu_q || !aligned(cu_q, 4) || (lse && !aligned(lse, 4)))
     return MK_ERR_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mk_attn_ws_bytes(head_dim))
     return MK_ERR_ARG;

@@ -87,9 +87,10 @@ int mk_qk_norm_rope(const mk_rope* rope, const void* q, int64_t q_ts, int64_t q_
   if (tokens == 0) return MK_OK;
   const int size = value_size(dtype);
   if (!positions || !aligned(positions, 4) || !rows_ok(q, q_ts, q_hs, size) ||
-      !rows_ok(q_out, qo_ts, qo_hs, size))
+      !out_rows_ok(q_out, qo_ts, qo_hs, tokens, q_heads, head_dim, size))
     return MK_ERR_ARG;
-  if (kv_heads > 0 && (!rows_ok(k, k_ts, k_hs, size) || !rows_ok(k_out, ko_ts, ko_hs, size)))
+  if (kv_heads > 0 && (!rows_ok(k, k_ts, k_hs, size) ||
+                       !out_rows_ok(k_out, ko_ts, ko_hs, tokens, kv_heads, head_dim, size)))
     return MK_ERR_ARG;
   if ((q_gain && !aligned(q_gain, 16)) || (k_gain && !aligned(k_gain, 16))) return MK_ERR_ARG;
   mk::rp::RopeArgs a;
@@ -171,6 +172,10 @@ int mk_kv_read(const mk_kv_cache* cache, const int64_t* slots, int tokens, void*
   unsigned blocks;
   const int rc = move_args(cache, k, k_ts, k_hs, v, v_ts, v_hs, slots, tokens, dtype, &a, &blocks);
   if (rc != MK_OK || tokens == 0) return rc;
+  const int size = value_size(dtype);
+  if (!out_rows_ok(k, k_ts, k_hs, tokens, cache->kv_heads, cache->head_dim, size) ||
+      !out_rows_ok(v, v_ts, v_hs, tokens, cache->kv_heads, cache->head_dim, size))
+    return MK_ERR_ARG;
   a.k_out = static_cast<unsigned char*>(k);
   a.v_out = static_cast<unsigned char*>(v);
   int status = MK_OK;

@@ -30,6 +30,13 @@ inline bool rows_ok(const void* p, int64_t ts, int64_t hs, int size) {
          (hs * size) % 16 == 0 && ts < (int64_t(1) << 38) && hs < (int64_t(1) << 38);
 }
 
+// Rows that a call writes: no two tokens or heads may share theirs.
+inline bool out_rows_ok(const void* p, int64_t ts, int64_t hs, int tokens, int heads, int head_dim,
+                        int size) {
+  return rows_ok(p, ts, hs, size) && (tokens == 1 || ts >= head_dim) &&
+         (heads == 1 || hs >= head_dim);
+}
+
 inline bool head_dim_ok(int hd) { return hd == 64 || hd == 128 || hd == 256; }
 
 // MK_OK and the kernels' view of a cache, or the error of a bad one.

@@ -371,7 +371,9 @@ int mk_gemv_w4(const void *codes, const float *scales, const float *x, int T,
  * `hs` are the distances between tokens and between heads in values (>= 0),
  * so that a slice of a fused projection's output is a valid argument, and with
  * a distance of 0 an input whose tokens or heads share rows (but for what the
- * attention calls say of it).  Rows
+ * attention calls say of it).  Rows that a call writes do not overlap: between
+ * several tokens or heads of an output (an input turned in place is one) the
+ * distance is head_dim or more (else MK_ERR_ARG).  Rows
  * start on 16-byte boundaries (base pointers and both distances; else
  * MK_ERR_ARG).  head_dim is 64, 128 or 256 (else MK_ERR_UNSUPPORTED).  A call
  * with no tokens (or an empty batch) does nothing. */

@@ -111,3 +111,32 @@ def test_paged_queries_that_share_rows(mk, kind, hd, heads):
                 mk.attn_packed(q, q[:, :2], q[:, :2], rows, got)
             torch.cuda.synchronize()
             assert bool((got == 7).all())
+
+
+@pytest.mark.parametrize("n,heads", [(1, 4), (5, 1), (5, 4), (70, 4)])
+def test_outputs_in_any_order(mk, n, heads):
+    """Outputs laid out [head][token][dim], of one token or of one head: the bits of
+    contiguous ones."""
+    hd = 64
+    gen = torch.Generator(device="cuda").manual_seed(n + heads)
+    q, k, v = (torch.randn(n, heads, hd, generator=gen, device="cuda").to(BF) for _ in "qkv")
+    cu, pos = torch.tensor([0, n], **I32), torch.arange(n, **I32)
+    pool, table, _ = make_paged(gen, [n], heads, hd, 16, BF)
+    cache, slots = mk.KvCache(*pool), table[0].long()[pos.long() // 16] * 16 + pos % 16
+
+    def outputs(turned):
+        a = [torch.full((heads, n, hd) if turned else (n, heads, hd), 9.0, dtype=BF, device="cuda")
+             for _ in range(6)]
+        return [x.transpose(0, 1) for x in a] if turned else a
+
+    sides = []
+    for turned in (False, True):
+        o = outputs(turned)
+        mk.qk_norm_rope(mk.Rope(64, 1e4), q, k, pos, o[0], o[1])
+        mk.kv_read(cache, slots, o[2], o[3])
+        mk.attn_packed(q, k, v, cu, o[4])
+        mk.attn_paged(q, cache, table, cu[1:], cu, o[5])
+        sides.append(o)
+    torch.cuda.synchronize()
+    for a, b in zip(*sides):
+        assert torch.equal(a, b)
