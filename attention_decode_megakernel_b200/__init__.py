@@ -618,16 +618,29 @@ def attn_workspace(head_dim, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _attn_outputs(shape, dtype, dev, out, lse, workspace):
+def _call_workspace(head_dim, dev, stream):
+    """A workspace for one call on `stream`.  It belongs to that stream in the allocator's
+    books, so that its memory is handed out again behind the call, in the stream's order."""
+    device = "cuda:%d" % dev
+    if stream is None:
+        return attn_workspace(head_dim, device)
+    if stream in (0, 1):  # names of the default stream (NULL, cudaStreamLegacy)
+        stream = _torch.cuda.default_stream(device)
+    else:
+        stream = _torch.cuda.ExternalStream(stream, device=device)
+    with _torch.cuda.stream(stream):
+        return attn_workspace(head_dim, device)
+
+
+def _attn_outputs(shape, dtype, dev, stream, out, lse, workspace):
+    """(pointer, distances of out, pointer of lse, the workspace: held until the call is made)"""
     op, ots, ohs = _rows(out, "out", shape, dtype, dev)
     lp = 0 if lse is None else _vector(lse, "lse", _torch.float32, (shape[0], shape[1]), dev)
     if workspace is None:
-        workspace = attn_workspace(shape[2], "cuda:%d" % dev)
+        workspace = _call_workspace(shape[2], dev, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the rows' device")
-    # (a workspace made here lives on as long as the call needs it: its memory is
-    # handed out again in the stream's order only)
-    return op, ots, ohs, lp, workspace.data_ptr(), workspace.nbytes
+    return op, ots, ohs, lp, workspace
 
 
 def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None, workspace=None,
@@ -655,9 +668,9 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     tp = _vector(block_table, "block_table", i32, (batch, pages), dev)
     sp = _vector(seq_lens, "seq_lens", i32, (batch,), dev)
     cp = _vector(cu_q, "cu_q", i32, (batch + 1,), dev)
-    op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
+    op, ots, ohs, lp, ws = _attn_outputs(shape, dtype, dev, stream, out, lse, workspace)
     _paged_call.slow(dev, stream, cache.address, qp, qts, qhs, tp, pages, sp, cp, op, ots, ohs, lp,
-                     rows, batch, heads, scale, code, wp, wn)
+                     rows, batch, heads, scale, code, ws.data_ptr(), ws.nbytes)
 
 
 def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, stream=None):
@@ -680,6 +693,6 @@ def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, 
     vp, vts, vhs = _rows(v, "v", kshape, dtype, dev)
     batch = cu_seqlens.shape[0] - 1
     cp = _vector(cu_seqlens, "cu_seqlens", _torch.int32, (batch + 1,), dev)
-    op, ots, ohs, lp, wp, wn = _attn_outputs(shape, dtype, dev, out, lse, workspace)
+    op, ots, ohs, lp, ws = _attn_outputs(shape, dtype, dev, stream, out, lse, workspace)
     _packed_call.slow(dev, stream, qp, qts, qhs, kp, kts, khs, vp, vts, vhs, cp, op, ots, ohs, lp,
-                      rows, batch, heads, kshape[1], hd, scale, code, wp, wn)
+                      rows, batch, heads, kshape[1], hd, scale, code, ws.data_ptr(), ws.nbytes)

@@ -140,3 +140,46 @@ def test_outputs_in_any_order(mk, n, heads):
     torch.cuda.synchronize()
     for a, b in zip(*sides):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("t", [1, 40])
+def test_own_workspace_on_another_stream(mk, kind, t):
+    """Calls on streams that are not the current one, without a workspace, while the current
+    one takes and fills memory: the bits of a call alone."""
+    gen = torch.Generator(device="cuda").manual_seed(t)
+    pool, table, _ = make_paged(gen, [5000, 900], 2, 128, 64, kind)
+    cache, lens = mk.KvCache(*pool), torch.tensor([5000, 900], **I32)
+    q = torch.randn(2 * t, 8, 128, generator=gen, device="cuda").to(BF)
+    k, v = (torch.randn(2 * t, 2, 128, generator=gen, device="cuda").to(BF) for _ in "kv")
+    cu = torch.tensor([0, t, 2 * t], **I32)
+
+    def both(a, b, **given):
+        mk.attn_paged(q, cache, table, lens, cu, a, **given)
+        mk.attn_packed(q, k, v, cu, b, **given)
+
+    want = [torch.empty_like(q) for _ in "ab"]
+    both(*want)
+    torch.cuda.synchronize()
+    size = mk.lib().mk_attn_ws_bytes(128)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    handles = [s.cuda_stream for s in streams] + [0]
+    got = [[torch.full_like(q, math.nan) for _ in "ab"] for _ in handles]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for out, h in zip(got, handles):
+            both(*out, stream=h)
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for out in got:
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    owners = {s["stream"] for s in torch.cuda.memory_snapshot() if s["total_size"] >= size}
+    assert owners >= set(handles[:2])
+    # and captured, by the handle of the stream that captures
+    out = [torch.full_like(q, math.nan) for _ in "ab"]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both(*out, stream=torch.cuda.current_stream().cuda_stream)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
