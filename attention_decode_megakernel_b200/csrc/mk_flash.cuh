@@ -821,6 +821,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&f.q_ready);
       }
+      // (plain loads of the table, codes and scales: this kernel is there before the one in
+      // front has written them, so they are not constant while it lives)
       // stage n of the segment in the order in which the issuer takes them
       const int len = at.s.len, j0 = at.j;
       auto what = [&](int n, bool& v, int& j, int& p) {
@@ -843,9 +845,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
         pc = x % per;
       };
       auto page_of = [&](int key) {
-        const int page = key < len ? __ldg(a.table + (long long)at.b * a.table_stride +
-                                           (key >> a.c.page_shift))
-                                   : -1;
+        const int page =
+            key < len ? a.table[(long long)at.b * a.table_stride + (key >> a.c.page_shift)] : -1;
         return page < a.c.n_pages ? page : -1;
       };
       auto load = [&](int n, uint4 (&w)[N]) {
@@ -861,9 +862,9 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
           const int page = page_of(key);
           w[i] = make_uint4(0, 0, 0, 0);
           if (page >= 0)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(
+            w[i] = *reinterpret_cast<const uint4*>(
                 src + page * a.c.page_stride + at.h * a.c.head_stride +
-                (key & (a.c.page_size - 1)) * a.c.pos_stride + (v ? 0 : p * F::KC * 64) + pc * 16));
+                (key & (a.c.page_size - 1)) * a.c.pos_stride + (v ? 0 : p * F::KC * 64) + pc * 16);
         }
       };
       uint4 cur[N], next[N];
@@ -880,8 +881,8 @@ __global__ void __launch_bounds__(FlashCfg<C, HD>::THREADS, 1)
             const long long at_scale =
                 (((long long)page * a.c.kv_heads + at.h) << a.c.page_shift) +
                 (key & (a.c.page_size - 1));
-            ks = __ldg(a.c.k_scale + at_scale);
-            vs = __ldg(a.c.v_scale + at_scale);
+            ks = a.c.k_scale[at_scale];
+            vs = a.c.v_scale[at_scale];
           }
         }
         if (n + 1 < 2 * seg * PARTS) load(n + 1, next);
