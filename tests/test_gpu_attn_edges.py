@@ -183,3 +183,55 @@ def test_own_workspace_on_another_stream(mk, kind, t):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_refused_calls_write_nothing(mk):
+    """Neither way of the binding launches anything for a call that it refuses: every
+    buffer that the call could have written keeps its bits."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    hq, hk, hd, n = 8, 2, 64, 10
+    x = torch.randn(n, hq + 2 * hk, hd, generator=gen, device="cuda").to(BF)
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    pos, slots = torch.arange(n, **I32), torch.arange(n, device="cuda")
+    pool = [torch.randn(2, hk, 16, hd, generator=gen, device="cuda").to(BF) for _ in "kv"]
+    cache, rope, ws = mk.KvCache(*pool), mk.Rope(64, 1e4), mk.attn_workspace(hd)
+    table, lens, cu = (torch.tensor(y, **I32) for y in ([[0, 1]], [n], [0, n]))
+    out, lse = torch.full((n, hq, hd), 3.0, dtype=BF, device="cuda"), torch.full((n, hq), 3.0,
+                                                                               device="cuda")
+    kb, vb = (torch.full((n, hk, hd), 3.0, dtype=BF, device="cuda") for _ in "kv")
+    written = [x, *pool, out, lse, kb, vb]
+    before = [y.clone() for y in written]
+    refused = [
+        lambda **s: mk.qk_norm_rope(rope, q, k, pos.long(), **s),
+        lambda **s: mk.qk_norm_rope(rope, q, k, pos[:9], **s),
+        lambda **s: mk.qk_norm_rope(rope, q, k[:5], pos, out, kb, **s),
+        lambda **s: mk.qk_norm_rope(rope, q, k, pos, out, kb[:, :1], **s),
+        lambda **s: mk.qk_norm_rope(rope, q, k, pos, out, kb, q_gain=ws[:64], **s),
+        lambda **s: mk.qk_norm_rope(rope, q, k, pos, out, kb, eps=-1.0, **s),
+        lambda **s: mk.qk_norm_rope(mk.Rope(128, 1e4), q, k, pos, out, kb, **s),
+        lambda **s: mk.kv_write(cache, k, v[:, :1], slots, **s),
+        lambda **s: mk.kv_write(cache, k, v, slots[:9], **s),
+        lambda **s: mk.kv_write(cache, q, q, slots, **s),
+        lambda **s: mk.kv_read(cache, slots.int(), kb, vb, **s),
+        lambda **s: mk.kv_read(cache, slots, kb, vb[:, :1].expand(-1, hk, -1), **s),
+        lambda **s: mk.attn_paged(q, cache, table.t(), lens, cu, out, lse, workspace=ws, **s),
+        lambda **s: mk.attn_paged(q, cache, table, lens, cu[:1], out, lse, workspace=ws, **s),
+        lambda **s: mk.attn_paged(q, cache, table, lens, cu, out[:9], lse, workspace=ws, **s),
+        lambda **s: mk.attn_paged(q, cache, table, lens, cu, out, lse[:, :7], workspace=ws, **s),
+        lambda **s: mk.attn_paged(q, cache, table, lens, cu, out, lse, workspace=ws[:4096], **s),
+        lambda **s: mk.attn_paged(q, cache, table, lens, cu, out, lse, scale=0.0, workspace=ws, **s),
+        lambda **s: mk.attn_packed(q, k, v[:9], cu, out, lse, workspace=ws, **s),
+        lambda **s: mk.attn_packed(q, k, v, cu.cpu(), out, lse, workspace=ws, **s),
+        lambda **s: mk.attn_packed(q, k, v, cu, out, lse, workspace=ws[:4096], **s),
+        lambda **s: mk.attn_packed(q[:, :7], k, v, cu, out[:, :7], lse[:, :7].contiguous(),
+                                   workspace=ws, **s)]
+    for given in ({}, dict(stream=torch.cuda.current_stream().cuda_stream)):
+        for i, call in enumerate(refused):
+            with pytest.raises((ValueError, mk.MkError)):
+                call(**given)
+            torch.cuda.synchronize()
+            for a, b in zip(written, before):
+                assert torch.equal(a, b), i
+    mk.attn_packed(q, k, v, cu, out, lse, workspace=ws)  # what they would have done
+    torch.cuda.synchronize()
+    assert not bool((out == 3).all()) and not bool((lse == 3).any())
