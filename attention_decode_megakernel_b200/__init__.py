@@ -407,8 +407,15 @@ def _code(dtype, what):
     return code
 
 
+def _counted(what, *numbers):
+    """What the C entries count in 32 bits (ctypes would cut a larger number)."""
+    if max(numbers) > 0x7FFFFFFF:
+        raise ValueError("%s: more than 2^31 - 1 in a dimension" % what)
+
+
 def _rows(t, what, shape, dtype, device):
     """(pointer, token distance, head distance) of a [token][head][dim] view."""
+    _counted(what, *shape)
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError("%s must be [token][head][dim] = %s of %s on the device of the other "
                          "rows, got %s of %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
@@ -664,6 +671,7 @@ def attn_paged(q, cache, block_table, seq_lens, cu_q, out, lse=None, scale=None,
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][pages]")
     batch, pages = block_table.shape
+    _counted("block_table", batch, pages)
     i32 = _torch.int32
     tp = _vector(block_table, "block_table", i32, (batch, pages), dev)
     sp = _vector(seq_lens, "seq_lens", i32, (batch,), dev)
@@ -692,6 +700,7 @@ def attn_packed(q, k, v, cu_seqlens, out, lse=None, scale=None, workspace=None, 
     kp, kts, khs = _rows(k, "k", kshape, dtype, dev)
     vp, vts, vhs = _rows(v, "v", kshape, dtype, dev)
     batch = cu_seqlens.shape[0] - 1
+    _counted("cu_seqlens", batch)
     cp = _vector(cu_seqlens, "cu_seqlens", _torch.int32, (batch + 1,), dev)
     op, ots, ohs, lp, ws = _attn_outputs(shape, dtype, dev, stream, out, lse, workspace)
     _packed_call.slow(dev, stream, qp, qts, qhs, kp, kts, khs, vp, vts, vhs, cp, op, ots, ohs, lp,

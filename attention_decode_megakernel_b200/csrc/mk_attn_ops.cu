@@ -15,7 +15,8 @@ int attn_args(const void* q, int64_t q_ts, int64_t q_hs, const int32_t* cu_q, vo
     return MK_ERR_ARG;
   if (!head_dim_ok(head_dim)) return MK_ERR_UNSUPPORTED;
   if (q_heads % kv_heads) return MK_ERR_ARG;
-  if (q_heads / kv_heads > 128) return MK_ERR_UNSUPPORTED;
+  // (more than 2^30 sequences: their numbers in rounds of 32 would pass 32 bits)
+  if (q_heads / kv_heads > 128 || batch > 1 << 30) return MK_ERR_UNSUPPORTED;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return MK_ERR_ARG;
   if (rows == 0 || batch == 0) return MK_OK;
   if (!rows_ok(q, q_ts, q_hs, 2) || !out_rows_ok(out, o_ts, o_hs, rows, q_heads, head_dim, 2) ||
@@ -252,7 +253,7 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   if (!block_table || !aligned(block_table, 4) || table_stride <= 0 || !seq_lens ||
       !aligned(seq_lens, 4))
     return MK_ERR_ARG;
-  const long long unit = (long long)a.group * ((rows + batch - 1) / batch);
+  const long long unit = a.group * (((long long)rows + batch - 1) / batch);
   if (unit > 16 && !walked(q_ts, rows, q_hs, q_heads)) return MK_ERR_UNSUPPORTED;
   a.table = block_table;
   a.table_stride = table_stride;

@@ -495,7 +495,8 @@ size_t mk_attn_ws_bytes(int head_dim);
  *   block_table device int32 [batch][table_stride]; seq_lens device int32
  *     [batch], held to 0 .. table_stride * page_size (and to 2^30); a page
  *     number outside the cache stands for keys and values of zero
- *   cu_q device int32 [batch + 1], from 0, not decreasing, at most `rows`;
+ *   cu_q device int32 [batch + 1], from 0, not decreasing, at most `rows`; batch
+ *     at most 2^30 (else MK_ERR_UNSUPPORTED);
  *     rows from cu_q[batch] on are left as they were
  *   lse device float32 [rows][q_heads] or NULL: the natural logarithm of the
  *     sum of exp(scale * q . k_j)
