@@ -377,7 +377,8 @@ def gemv_w4(codes, scales, x, y, stream=None):
 #
 # Tensors are device tensors; rows are [token][head][dim] views with any token
 # and head distance (a slice of a fused projection, say).  Without `stream` a
-# call runs on torch's current stream of the tensors' device.
+# call runs on torch's current stream of the tensors' device.  The calls serve
+# only: they record nothing for autograd, whatever requires a gradient.
 #
 # A decoded token's calls take a few microseconds on the device, less than
 # Python needs to look at seven tensors.  So a call first goes, as it is, to

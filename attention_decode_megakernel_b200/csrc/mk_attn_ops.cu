@@ -65,11 +65,11 @@ int device_sms(int* dev, int* sms) {
   return MK_OK;
 }
 
-// What a unit costs besides its key tiles, in key tiles (mk_split.cuh), by sweeps: two
-// for tiles of rows (8 prompts of up to 4096 tokens at head_dim 128: 385 us at 0, 366 at 1,
-// 364 at 2, 377 at 4), two for few rows (64 sequences of up to 4096 over an e4m3 cache:
-// 39.6 us at 0, 38.4 at 1, 36.0 at 2, 35.7 at 3, 36.2 at 4; at head_dim 128 31.3, 30.4, 28.7,
-// 29.3, 30.2).
+// What a unit costs besides its key tiles, in key tiles (mk_split.cuh), by sweeps in long
+// runs, under the power cap: two for tiles of rows (8 prompts of up to 4096 tokens at head_dim
+// 128: 428 us at 0, 412 at 1, 407 at 2, 411 at 3, 415 at 4), two for few rows (64 sequences of
+// up to 4096 over an e4m3 cache: 40.8 us at 0, 39.5 at 1, 36.9 at 2, 36.6 at 3, 37.2 at 4;
+// at head_dim 128 31.8, 31.2, 29.3, 30.1, 31.0).
 constexpr int kFewExtra = 2, kFlashExtra = 2;
 
 // Calls whose sequences hold at most so many keys do not divide units over CTAs, and
@@ -77,7 +77,8 @@ constexpr int kFewExtra = 2, kFlashExtra = 2;
 // tokens 13.8 / 15.4 us, of 780 17.1 / 17.0; 5 tokens over 128 keys 8.7 / 12.0, over 260
 // 11.8 / 12.4, over 520 15.5 / 12.3; one token over 64 keys 5.1 / 7.1, over 128 6.1 / 6.9,
 // over 260 9.0 / 7.2.  (64 sequences of exactly 520 would gain too, 14.6 / 17.5, but not
-// ragged ones, and the call knows no more than the longest.)
+// ragged ones, and the call knows no more than the longest.)  The longest is what the table
+// (of a packed call, its rows) has room for: the lengths are on the device.
 constexpr int kWholePrompt = 640, kWholeChunk = 256, kWholeFew = 128;
 
 // cuTensorMapEncodeTiled through the runtime (no link against the driver library).
@@ -262,6 +263,10 @@ int mk_attn_paged(const mk_kv_cache* cache, const void* q, int64_t q_ts, int64_t
   rc = device_sms(&dev, &sms);
   if (rc != MK_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // By the rows of a unit on average: up to 8 or 16 the few-row kernel. It serves the whole
+  // batch, so that one chunk of 512 among 256 single tokens walks its keys four tokens at a
+  // time (contexts of up to 8192, 8 + 2 heads of 256: 774 us, 427 + 40 as two calls; 16 + 4
+  // heads of 128: 524, 420 + 48).
   const long long longest = (long long)table_stride * cache->page_size;
   by_half_type(dtype, [&](auto t) {
     by_head_dim(cache->head_dim, [&](auto d) {

@@ -15,7 +15,10 @@
 // on one tile, the tensor cores run the other stream's products (or the next tile's
 // scores and the last one's output).  The maximum of a row is raised only when a score
 // passes it by far (mk_paged.cuh, Weights), and only then is O rescaled in TMEM;
-// the sum of weights is kept in fp32 from the unrounded weights.
+// the sum of weights is kept in fp32 from the unrounded weights.  The weights' rounding to
+// 16 bits is what the tensor cores' rate costs (operands in 32 bits would halve it and double
+// V): in bf16 the root mean square error of the outputs is 2.3e-3 of them, 1.7e-3 with
+// exact weights, which is the outputs' own rounding.
 //
 // K and V tiles: one TMA box of 64 dims by min(page, 128) positions each, the
 // page looked up by the producer's lanes; boxes behind the last key and of
@@ -24,7 +27,9 @@
 // scores are masked, but 0 * NaN is NaN).  An e4m3 cache has a warpgroup
 // of converters in the producer's place: codes through registers to fp16
 // tiles, exactly, the rows' scales beside them; queries become fp16 after a
-// power of two for each row.
+// power of two for each row.  The converters set the pace there: each piece is a page
+// lookup and a load behind it, one stage ahead (1024 tokens at 32768 keys, e4m3 / bf16: 219 /
+// 105 us at head_dim 64, 1240 / 267 at 128, 2010 / 255 at 256).
 //
 // Every wait is bounded; one that runs out makes the CTA write NaN.
 #pragma once

@@ -452,7 +452,8 @@ typedef struct {
 /* Write the rows of `tokens` tokens into a cache: token t goes to slot
  * slots[t] = page * page_size + position (device int64 [tokens]); a slot
  * outside the cache (-1 for padding) skips its token.  Slots of one call are
- * distinct: of two tokens with one slot, either may be kept.  k, v device
+ * distinct: two tokens with one slot leave a mixture of their rows and scales
+ * there, and nothing else is touched.  k, v device
  * [tokens][kv_heads][head_dim] of dtype MK_BF16, MK_FP16 or MK_FP32, rounded
  * to nearest even.  For an e4m3 cache the scale of a row is the least power of
  * two, 2^-64 at least, that brings its largest magnitude to 448 or below;
@@ -504,8 +505,10 @@ size_t mk_attn_ws_bytes(int head_dim);
  * What lies behind seq_lens[b] in a page is never part of a result, whatever
  * its bits; a key that a token does not see within seq_lens[b] must have
  * finite values.  out must not overlap an input.  Results do not depend on
- * timing: the same call gives the same bits.  Device-side waits are bounded
- * (2 s): rows of a tile whose wait runs out are set to NaN. */
+ * timing: the same call gives the same bits.  One kernel, chosen by the mean
+ * number of new tokens (rows / batch), serves the whole batch: a long chunk
+ * beside many single tokens is faster as a call of its own.  Device-side waits
+ * are bounded (2 s): rows of a tile whose wait runs out are set to NaN. */
 int mk_attn_paged(const mk_kv_cache *cache, const void *q, int64_t q_ts,
                   int64_t q_hs, const int32_t *block_table, int table_stride,
                   const int32_t *seq_lens, const int32_t *cu_q, void *out,
